@@ -1,7 +1,7 @@
 /*
  * moe.h -- C ABI of the B200 (sm_100a) quantized Mixture-of-Experts FFN layer.
  *
- * Three calls:
+ * The layer in three calls:
  *   moe_pack           quantizes fp32 expert weights into the packed layer buffer
  *                      (optionally keeping each matrix's largest weights in an
  *                      fp16 side list);
@@ -10,6 +10,9 @@
  *                      per-expert SwiGLU FFN on dequantized weights -> weighted
  *                      combine;
  *   moe_layer_forward_noalloc  the same with a workspace inside the library.
+ * Around it, for experts and adapters that the caller runs: moe_sort, moe_dispatch and
+ * moe_collect with their gradients, 8-bit activation checkpoints (moe_act_*,
+ * moe_swiglu_*) and moe_adapters (second half of this file).
  *
  * Where the method comes from (web pages; section numbers as printed there):
  *  - "quantized MoE LLM inference" (cloud.baidu.com article 9434801), expert
@@ -344,6 +347,140 @@ MOE_API moe_status moe_layer_forward(const void* x, int32_t T, const float* rout
 MOE_API moe_status moe_layer_forward_noalloc(const void* x, int32_t T, const float* router_w,
                                              const float* router_b, const moe_weights* w, int32_t k, void* y,
                                              const moe_debug* dbg, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the expert products, for callers that run experts of their
+ * own next to the layer (16-bit experts while fine-tuning, expert parallelism,
+ * adapters over a frozen packed layer).  They follow the conventions at the top
+ * of this file.  Matrices are row-major with a pitch in values (ld >= columns)
+ * and any alignment that their type has; where the pointers, pitches and widths
+ * allow 16-byte access it is used.  Offsets are 64-bit.  Outputs must not
+ * overlap inputs unless a call says so.  All sums are fp32 in a fixed order, so
+ * results are the same from call to call; a value is rounded once, when stored.
+ */
+
+/* Value types of the operators. */
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+#define MOE_MAX_GROUPS 1024 /* experts, or adapters, of a sort */
+
+/*
+ * moe_sort -- the T*k entries i = t*k+j sorted by group (the layer's permutation
+ * of tokens by expert, expert-routing section of the quantized MoE inference page).
+ *
+ * idx: DEVICE i32 [T][k].  An entry outside [0, E) has no group and is dropped
+ *   (padding tokens: -1).
+ * perm: DEVICE i32 [T*k]; perm[row] = entry.  Groups ascending, the entries of a
+ *   group ascending, then the dropped entries ascending.
+ * inv: DEVICE i32 [T*k]; inv[entry] = row, -1 for a dropped entry.
+ * offsets: DEVICE i32 [E+1]; group e has rows [offsets[e], offsets[e+1]);
+ *   offsets[E] = rows that have a group.
+ * ws: DEVICE, 256-byte aligned; ws == NULL -> *ws_bytes_out = the size needed
+ *   for (T, k, E) and nothing runs.
+ * Limits: 1 <= k <= 8, T*k <= 2^20, 1 <= E <= MOE_MAX_GROUPS.
+ * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_SHAPE, MOE_ERR_WORKSPACE,
+ *   MOE_ERR_UNSUPPORTED_DEVICE, MOE_ERR_CUDA (those of every operator below too).
+ */
+MOE_API moe_status moe_sort(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* perm, int32_t* inv,
+                            int32_t* offsets, void* ws, uint64_t ws_bytes, uint64_t* ws_bytes_out,
+                            cudaStream_t stream);
+
+/*
+ * moe_dispatch -- moe_sort, and the tokens' rows in that order:
+ *   xs[row] = x[perm[row] / k] for row < offsets[E]; the rows behind stay as they were.
+ * x: DEVICE [T][H], xs: DEVICE [T*k][H], both of `dtype` (MOE_BF16, ...; unknown:
+ *   MOE_ERR_FORMAT).  1 <= H <= 2^20.
+ */
+MOE_API moe_status moe_dispatch(const void* x, int64_t ldx, int32_t dtype, const int32_t* idx, int32_t T, int32_t k,
+                                int32_t E, int32_t H, void* xs, int64_t ldxs, int32_t* perm, int32_t* inv,
+                                int32_t* offsets, void* ws, uint64_t ws_bytes, uint64_t* ws_bytes_out,
+                                cudaStream_t stream);
+
+/*
+ * moe_dispatch_backward -- dx[t] = sum over j of dxs[inv[t*k+j]], dropped entries left
+ *   out (a token without any gets zeros).  dxs: DEVICE [T*k][H]; rows that inv does not
+ *   name are not read.  An inv outside [0, T*k) counts as dropped.
+ */
+MOE_API moe_status moe_dispatch_backward(const void* dxs, int64_t lddxs, int32_t dtype, const int32_t* inv, int32_t T,
+                                         int32_t k, int32_t H, void* dx, int64_t lddx, cudaStream_t stream);
+
+/*
+ * moe_collect -- y[t] = sum over j ascending of w[t*k+j] * o[inv[t*k+j]] (the layer's
+ *   weighted combine).  w: DEVICE fp32 [T][k], not read for dropped entries.
+ */
+MOE_API moe_status moe_collect(const void* o, int64_t ldo, int32_t dtype, const float* w, const int32_t* inv, int32_t T,
+                               int32_t k, int32_t H, void* y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * moe_collect_backward -- the gradients of moe_collect:
+ *   d_o[inv[t*k+j]] = w[t*k+j] * dy[t];  dw[t*k+j] = <dy[t], o[inv[t*k+j]]> (fp32; 0 for a
+ *   dropped entry).  Rows of d_o that inv does not name stay as they were.
+ */
+MOE_API moe_status moe_collect_backward(const void* dy, int64_t lddy, const void* o, int64_t ldo, int32_t dtype,
+                                        const float* w, const int32_t* inv, int32_t T, int32_t k, int32_t H, void* d_o,
+                                        int64_t lddo, float* dw, cudaStream_t stream);
+
+/*
+ * moe_act_save -- an activation kept in 8 bits for a backward pass.
+ *
+ * Per row and group of 32 consecutive columns (the last may be shorter): e = the
+ *   smallest whole number with max|x| <= 127 * 2^e, at least -126 and at most 121
+ *   (fp16 values: 9); q = rint(x * 2^-e), half to even, clamped to [-127, 127].
+ * codes: DEVICE i8 [R][F].  exps: DEVICE u8 [R][ceil(F/32)], e + 127; 255 with zero
+ *   codes for a group that holds an infinity or a NaN.
+ * n_rows: DEVICE i32 [1] or NULL: only rows below *n_rows are read and written (for
+ *   example offsets + E of a sort).
+ * 1 <= F <= 2^20; R * ceil(F/32) < 2^31 - 64.
+ */
+MOE_API moe_status moe_act_save(const void* x, int64_t ldx, int32_t dtype, int32_t R, int32_t F, int8_t* codes,
+                                uint8_t* exps, const int32_t* n_rows, cudaStream_t stream);
+
+/*
+ * moe_act_load -- x = q * 2^e, rounded to `dtype` (exact in fp32, and in the type that was
+ *   saved); NaN throughout a group with exponent byte 255.
+ */
+MOE_API moe_status moe_act_load(const int8_t* codes, const uint8_t* exps, int32_t R, int32_t F, int32_t dtype, void* x,
+                                int64_t ldx, const int32_t* n_rows, cudaStream_t stream);
+
+/*
+ * moe_swiglu_save -- h = silu(g) * u (the layer's activation) and what its backward pass
+ *   needs, g and u in 8 bits as moe_act_save keeps them.
+ */
+MOE_API moe_status moe_swiglu_save(const void* g, int64_t ldg, const void* u, int64_t ldu, int32_t dtype, int32_t R,
+                                   int32_t F, void* h, int64_t ldh, int8_t* g_codes, uint8_t* g_exps, int8_t* u_codes,
+                                   uint8_t* u_exps, const int32_t* n_rows, cudaStream_t stream);
+
+/*
+ * moe_swiglu_backward -- from the restored g, u and dh, with s = 1/(1+exp(-g)):
+ *   du = dh * g*s;  dg = dh * u * s*(1 + g*(1-s));  h = g*s * u (h == NULL: not made), the
+ *   activation again for the down projection's weight gradient.
+ */
+MOE_API moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t dtype, const int8_t* g_codes,
+                                       const uint8_t* g_exps, const int8_t* u_codes, const uint8_t* u_exps, int32_t R,
+                                       int32_t F, void* dg, int64_t lddg, void* du, int64_t lddu, void* h, int64_t ldh,
+                                       const int32_t* n_rows, cudaStream_t stream);
+
+/*
+ * moe_adapters -- low-rank adapters of many requests beside a shared projection or the
+ *   whole layer: out[t] = y[t] + scale[a] * B[a] (A[a] x[t]) for the adapter a of token t,
+ *   out[t] = y[t] for a token without one.
+ *
+ * x: DEVICE [T][K]; y, out: DEVICE [T][N], out may be y (then rows without an adapter
+ *   are not touched) and may not overlap anything otherwise.
+ * A: DEVICE [n][r][K], B: DEVICE [n][N][r], contiguous, of `dtype` (MOE_BF16 or MOE_F16;
+ *   MOE_F32: MOE_ERR_FORMAT).  An adapter of a smaller rank is padded with zeros.
+ * scale: DEVICE fp32 [n].
+ * perm, offsets: moe_sort of the tokens' adapters (k = 1, E = n, -1: none); one sort
+ *   serves every layer of a step.  An entry of perm outside [0, T) is skipped.
+ * Limits: T <= 2^20; 1 <= n <= MOE_MAX_GROUPS; r a multiple of 8 up to 128; K and N
+ *   multiples of 8 from 8 to 2^20.  All matrices 16-byte aligned, pitches multiples of
+ *   8 values (MOE_ERR_ALIGN).
+ * ws as for moe_sort; its size depends on (T, K, r, n).
+ */
+MOE_API moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
+                                int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
+                                const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
+                                int64_t ldo, void* ws, uint64_t ws_bytes, uint64_t* ws_bytes_out, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,7 +23,9 @@ STATUS = {
     9: "MOE_ERR_RANGE",
 }
 
-EXPORTS = ("moe_pack", "moe_layer_forward", "moe_layer_forward_noalloc")
+EXPORTS = ("moe_pack", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_sort", "moe_dispatch",
+           "moe_dispatch_backward", "moe_collect", "moe_collect_backward", "moe_act_save", "moe_act_load",
+           "moe_swiglu_save", "moe_swiglu_backward", "moe_adapters")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -68,6 +70,22 @@ def load() -> C.CDLL:
         L.moe_layer_forward_noalloc.restype = C.c_int
         L.moe_layer_forward_noalloc.argtypes = [P, i32, P, P, C.POINTER(MoeWeights), i32, P,
                                                 C.POINTER(MoeDebug), P]
+        i64 = C.c_int64
+        ws = [P, u64, P, P]  # workspace, its bytes, bytes needed, stream
+        for name, args in {
+            "moe_sort": [P, i32, i32, i32, P, P, P, *ws],
+            "moe_dispatch": [P, i64, i32, P, i32, i32, i32, i32, P, i64, P, P, P, *ws],
+            "moe_dispatch_backward": [P, i64, i32, P, i32, i32, i32, P, i64, P],
+            "moe_collect": [P, i64, i32, P, P, i32, i32, i32, P, i64, P],
+            "moe_collect_backward": [P, i64, P, i64, i32, P, P, i32, i32, i32, P, i64, P, P],
+            "moe_act_save": [P, i64, i32, i32, i32, P, P, P, P],
+            "moe_act_load": [P, P, i32, i32, i32, P, i64, P, P],
+            "moe_swiglu_save": [P, i64, P, i64, i32, i32, i32, P, i64, P, P, P, P, P, P],
+            "moe_swiglu_backward": [P, i64, i32, P, P, P, P, i32, i32, P, i64, P, i64, P, i64, P, P],
+            "moe_adapters": [P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, i64, *ws],
+        }.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = C.c_int, args
         _lib = L
     return _lib
 

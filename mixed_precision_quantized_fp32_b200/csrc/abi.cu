@@ -7,9 +7,9 @@
 
 namespace moe {
 namespace {
-
 constexpr int kMaxDev = 64;
 int g_dev_ok[kMaxDev];  // 0 unknown, 1 sm_100, -1 other (per-process property cache)
+}  // namespace
 
 moe_status check_device() {
   int dev = 0;
@@ -25,6 +25,8 @@ moe_status check_device() {
   }
   return g_dev_ok[dev] == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
 }
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 

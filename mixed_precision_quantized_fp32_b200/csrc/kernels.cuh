@@ -4,6 +4,9 @@
 
 namespace moe {
 
+// MOE_OK if the current device runs this library (host ABI, abi.cu).
+moe_status check_device();
+
 // fmt_host: the caller's codes (MOE_FMT_OUTLIERS kept); out_sec / side_off: the outlier
 // section and side-list offsets (0 when absent).
 cudaError_t launch_pack(const float* W, int e0, int ne, int E, int H, int F, const uint8_t* fmt_host,

@@ -1,0 +1,132 @@
+// Shared by the operators around the expert products (routes.cu, ckpt8.cu,
+// adapters.cu): value types, vector loads and stores, and the launchers that the
+// host ABI (ops_abi.cu) calls.  All arithmetic is in fp32; a value is rounded once
+// (to nearest even) when it is stored in a 16-bit type.
+#pragma once
+#include "moe_common.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------- value types
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// N consecutive values <-> fp32 registers.  N = 1 asks for the type's own alignment,
+// any other N for 16 bytes.
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = to_f32<T>(__ldg(p));
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        v[8 * i + 2 * j] = f.x, v[8 * i + 2 * j + 1] = f.y;
+      }
+    }
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    *p = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+      reinterpret_cast<uint4*>(p)[i] =
+          make_uint4(pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
+                     pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+inline int dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// A row-major matrix as the operators take it: `ld` values from one row to the next.
+struct ConstRows {
+  const void* p;
+  int64_t ld;
+};
+struct Rows {
+  void* p;
+  int64_t ld;
+};
+
+constexpr int kMaxGroups = 1024;  // groups of a sort: experts, or the adapters of a bank
+
+// ---------------------------------------------------------------- launchers
+// Entries (t, j) sorted by group: workspace bytes and the launch; with x the rows follow.
+uint64_t sort_ws_bytes(int R, int E);
+cudaError_t launch_dispatch(const int32_t* idx, int T, int k, int E, int32_t* perm, int32_t* inv, int32_t* offsets,
+                            ConstRows x, Rows xs, int H, int dtype, void* ws, cudaStream_t stream);
+// y[t] = sum_j w[t,j] * o[inv[t,j]] (w null: 1)
+cudaError_t launch_collect(ConstRows o, const float* w, const int32_t* inv, int T, int k, int H, int dtype, Rows y,
+                           cudaStream_t stream);
+cudaError_t launch_collect_backward(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T, int k, int H,
+                                    int dtype, Rows d_o, float* dw, cudaStream_t stream);
+
+
+// 8-bit checkpoints (codes [R][F], exps [R][ceil(F/32)]); n_rows null: all R rows.
+struct Ckpt {
+  int8_t* q;
+  uint8_t* e;
+};
+cudaError_t launch_act_save(ConstRows x, int dtype, int R, int F, Ckpt c, const int32_t* n_rows, cudaStream_t stream);
+cudaError_t launch_act_load(Ckpt c, int R, int F, int dtype, Rows x, const int32_t* n_rows, cudaStream_t stream);
+cudaError_t launch_swiglu_save(ConstRows g, ConstRows u, int dtype, int R, int F, Rows h, Ckpt cg, Ckpt cu,
+                               const int32_t* n_rows, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(ConstRows dh, int dtype, Ckpt cg, Ckpt cu, int R, int F, Rows dg, Rows du, Rows h,
+                                   const int32_t* n_rows, cudaStream_t stream);
+
+// out = y + scale * B (A x) per token's adapter; out.p == y.p: in place.
+struct AdapterArgs {
+  ConstRows x, y;
+  Rows out;
+  int T, K, N, r, n;
+  const void *A, *B;
+  const float* scale;
+  const int32_t *perm, *offsets;
+  float* part;
+};
+uint64_t adapters_ws_bytes(int T, int K, int r, int n);
+cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t stream);
+
+}  // namespace moe

@@ -1,0 +1,376 @@
+// Rows sorted by expert and brought back: the permutation, gather and combine of the
+// layer forward as operators of their own, with their gradients (expert-routing section
+// of the quantized MoE inference page: tokens go to their chosen experts and the output
+// is the weighted sum of what the experts return).
+//
+//   sort             key(i) = idx[i] if 0 <= idx[i] < E, else E (dropped); a stable order
+//                    of the entries i = t*k + j by key
+//   dispatch         xs[row] = x[perm[row] / k]                  row < offsets[E]
+//   its gradient     dx[t]   = sum_j dxs[inv[t,j]]               (collect with weights 1)
+//   collect          y[t]    = sum_j w[t,j] * o[inv[t,j]]        ascending j, fp32
+//   its gradient     do[inv[t,j]] = w[t,j] * dy[t],  dw[t,j] = <dy[t], o[inv[t,j]]>
+//
+// Every kernel moves rows and computes next to nothing on them, so memory bounds it.
+// Rows are walked token by token: a token's row is read (or written) once, its k expert
+// rows once each, and nothing is accumulated in memory, so results do not depend on the
+// order in which blocks run.
+#include "ops_common.cuh"
+
+namespace moe {
+
+constexpr int kSortSmall = 1024;   // entries that one launch sorts by counting
+constexpr int kSortBlock = 1024;
+constexpr int kSortMaxBlocks = 128;
+
+__device__ __forceinline__ int sort_key(int32_t e, int E) { return (unsigned)e < (unsigned)E ? e : E; }
+
+// Copy one row of n units from src to dst; U is the widest unit that fits the pointers,
+// the pitches and the row.
+template <typename U>
+__device__ __forceinline__ void copy_row(const U* __restrict__ src, U* __restrict__ dst, int n) {
+  for (int c = threadIdx.x; c < n; c += blockDim.x) dst[c] = __ldg(src + c);
+}
+
+// Up to 1024 entries in one launch: the row of entry i is the number of entries with a
+// smaller key plus that of equal keys before it, so each block counts its own entry's
+// row (every thread looks at up to four keys) and copies its token's row there.  Block 0
+// makes the offsets.  At these sizes latency is all there is: one launch instead of
+// sort and gather behind one another.
+template <typename U>
+__global__ void __launch_bounds__(256) dispatch_small_kernel(const int32_t* __restrict__ idx, int R, int k, int E,
+                                                             int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+                                                             int32_t* __restrict__ offsets, const U* __restrict__ x,
+                                                             int64_t ldx, U* __restrict__ xs, int64_t ldxs, int n) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    __shared__ int32_t hist[kMaxGroups + 1];
+    __shared__ int32_t wsum[8];
+    for (int e = tid; e <= E; e += 256) hist[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < R; i += 256) atomicAdd(&hist[sort_key(idx[i], E)], 1);  // integer counts: any order
+    __syncthreads();
+    int run = 0;
+    for (int e0 = 0; e0 <= E; e0 += 256) {  // exclusive scan, 256 groups at a time
+      const int e = e0 + tid;
+      const int v = e <= E ? hist[e] : 0;
+      int s = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if ((tid & 31) >= o) s += u;
+      }
+      if ((tid & 31) == 31) wsum[tid >> 5] = s;
+      __syncthreads();
+      int before = run;
+      for (int w = 0; w < (tid >> 5); ++w) before += wsum[w];
+      if (e <= E) offsets[e] = before + s - v;
+      for (int w = 0; w < 8; ++w) run += wsum[w];
+      __syncthreads();
+    }
+    return;
+  }
+  const int i = blockIdx.x - 1;
+  const int key = sort_key(idx[i], E);
+  int row = 0;
+  for (int j0 = 0; j0 < R; j0 += 256) {
+    const int j = j0 + tid;
+    int before = 0;
+    if (j < R) {
+      const int kj = sort_key(idx[j], E);
+      before = kj < key || (kj == key && j < i);
+    }
+    row += __syncthreads_count(before);
+  }
+  if (tid == 0) {
+    perm[row] = i;
+    inv[i] = key < E ? row : -1;
+  }
+  if (x && key < E) copy_row(x + (int64_t)(i / k) * ldx, xs + (int64_t)row * ldxs, n);
+}
+
+// Pass 1 over `per` entries a block: histogram of the keys.
+__global__ void __launch_bounds__(kSortBlock) sort_hist_kernel(const int32_t* __restrict__ idx, int R, int per, int E,
+                                                               int32_t* __restrict__ blk_hist) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  __shared__ int32_t hist[kMaxGroups + 1];
+  for (int e = threadIdx.x; e <= E; e += kSortBlock) hist[e] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * per, hi = min(R, lo + per);
+  for (int i = lo + threadIdx.x; i < hi; i += kSortBlock) atomicAdd(&hist[sort_key(idx[i], E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kSortBlock) blk_hist[(size_t)blockIdx.x * (E + 1) + e] = hist[e];
+}
+
+// Pass 2: every block sums the histograms before its own (and all of them, for the
+// offsets), then ranks its entries 1024 at a time: rank = entries of the key in earlier
+// warps + lower lanes with the key.
+__global__ void __launch_bounds__(kSortBlock) sort_rank_kernel(const int32_t* __restrict__ idx, int R, int per, int E,
+                                                               const int32_t* __restrict__ blk_hist,
+                                                               int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+                                                               int32_t* __restrict__ offsets) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  extern __shared__ uint8_t wcnt[];  // [32][E+1]: entries of each key in each warp
+  __shared__ int32_t base[kMaxGroups + 1];
+  __shared__ int32_t wsum[kSortBlock / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int run = 0;
+  for (int e0 = 0; e0 <= E; e0 += kSortBlock) {
+    const int e = e0 + tid;
+    int total = 0, mine = 0;
+    if (e <= E) {
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int v = __ldg(blk_hist + (size_t)b * (E + 1) + e);
+        total += v;
+        mine += b < (int)blockIdx.x ? v : 0;
+      }
+    }
+    int s = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    int before = run;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (e <= E) {
+      const int off = before + s - total;
+      base[e] = off + mine;
+      if (blockIdx.x == 0) offsets[e] = off;
+    }
+    for (int w = 0; w < kSortBlock / 32; ++w) run += wsum[w];
+    __syncthreads();
+  }
+  const int lo = blockIdx.x * per, hi = min(R, lo + per);
+  for (int i0 = lo; i0 < hi; i0 += kSortBlock) {
+    for (int c = tid; c < 8 * (E + 1); c += kSortBlock) reinterpret_cast<uint32_t*>(wcnt)[c] = 0;  // 32 * (E+1) bytes
+    __syncthreads();
+    const int i = i0 + tid;
+    const int key = i < hi ? sort_key(idx[i], E) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const int below = __popc(same & ((1u << lane) - 1u));
+    if (key >= 0 && below == 0) wcnt[warp * (E + 1) + key] = (uint8_t)__popc(same);
+    __syncthreads();
+    if (key >= 0) {
+      int row = base[key] + below;
+      for (int w = 0; w < warp; ++w) row += wcnt[w * (E + 1) + key];
+      perm[row] = i;
+      inv[i] = key < E ? row : -1;
+    }
+    __syncthreads();
+    for (int e = tid; e <= E; e += kSortBlock) {
+      int s = 0;
+      for (int w = 0; w < kSortBlock / 32; ++w) s += wcnt[w * (E + 1) + e];
+      base[e] += s;
+    }
+    __syncthreads();
+  }
+}
+
+// One block per token: its row goes to each of its experts' rows.
+template <typename U>
+__global__ void __launch_bounds__(256) dispatch_rows_kernel(const U* __restrict__ x, int64_t ldx,
+                                                            const int32_t* __restrict__ inv, int k, U* __restrict__ xs,
+                                                            int64_t ldxs, int n) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  const int t = blockIdx.x;
+  int rows[kMaxK];
+  for (int j = 0; j < k; ++j) rows[j] = inv[(int64_t)t * k + j];
+  const U* src = x + (int64_t)t * ldx;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    const U v = __ldg(src + c);
+    for (int j = 0; j < k; ++j)
+      if (rows[j] >= 0) xs[(int64_t)rows[j] * ldxs + c] = v;
+  }
+}
+
+// Sum of a token's expert rows, weighted or not.
+template <typename T, int N>
+__global__ void __launch_bounds__(256) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
+                                                           const float* __restrict__ w,
+                                                           const int32_t* __restrict__ inv, int R, int k, int H,
+                                                           T* __restrict__ y, int64_t ldy) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  const int64_t t = blockIdx.x;
+  int rows[kMaxK];
+  float wt[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    rows[j] = j < k ? inv[t * k + j] : -1;
+    if ((unsigned)rows[j] >= (unsigned)R) rows[j] = -1;
+    wt[j] = (w && rows[j] >= 0) ? w[t * k + j] : 1.0f;
+  }
+  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * N; c < H; c += gridDim.y * blockDim.x * N) {
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {
+      if (rows[j] < 0) continue;
+      float v[N];
+      load_vec<T, N>(o + (int64_t)rows[j] * ldo + c, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[j], v[i], acc[i]);
+    }
+    store_vec<T, N>(y + t * ldy + c, acc);
+  }
+}
+
+// Gradient of collect: dy's row is read once, scaled into each expert row, and its dot
+// product with each expert's output summed over the block in a fixed order.
+template <typename T, int N>
+__global__ void __launch_bounds__(512) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
+                                                               const T* __restrict__ o, int64_t ldo,
+                                                               const float* __restrict__ w,
+                                                               const int32_t* __restrict__ inv, int R, int k, int H,
+                                                               T* __restrict__ d_o, int64_t lddo,
+                                                               float* __restrict__ dw) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  __shared__ float part[16][kMaxK];
+  const int64_t t = blockIdx.x;
+  int rows[kMaxK];
+  float wt[kMaxK], dot[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    rows[j] = j < k ? inv[t * k + j] : -1;
+    if ((unsigned)rows[j] >= (unsigned)R) rows[j] = -1;
+    wt[j] = rows[j] >= 0 ? w[t * k + j] : 0.0f;
+    dot[j] = 0.0f;
+  }
+  for (int c = threadIdx.x * N; c < H; c += blockDim.x * N) {
+    float g[N];
+    load_vec<T, N>(dy + t * lddy + c, g);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) {
+      if (rows[j] < 0) continue;
+      float v[N], d[N];
+      load_vec<T, N>(o + (int64_t)rows[j] * ldo + c, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dot[j] = fmaf(g[i], v[i], dot[j]);
+        d[i] = wt[j] * g[i];
+      }
+      store_vec<T, N>(d_o + (int64_t)rows[j] * lddo + c, d);
+    }
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    if (j >= k) break;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+    if (lane == 0) part[warp][j] = dot[j];
+  }
+  __syncthreads();
+  if (threadIdx.x < k) {
+    float s = 0.0f;
+    for (int q = 0; q < (int)(blockDim.x >> 5); ++q) s += part[q][threadIdx.x];
+    dw[t * k + threadIdx.x] = s;
+  }
+}
+
+// ---------------------------------------------------------------- host
+namespace {
+
+int sort_per_block(int R) {  // entries per block: a multiple of 1024, at most 128 blocks
+  const int per = (R + kSortMaxBlocks - 1) / kSortMaxBlocks;
+  return (per + kSortBlock - 1) / kSortBlock * kSortBlock;
+}
+
+template <typename U>
+cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, int32_t* inv, int32_t* offsets,
+                        ConstRows x, Rows xs, int es, int H, void* ws, cudaStream_t stream) {
+  const int R = T * k;
+  const int unit = sizeof(U);
+  const int64_t ldx = x.ld * es / unit, ldxs = xs.ld * es / unit;
+  const int n = (int)((int64_t)H * es / unit);
+  const U* xp = (const U*)x.p;
+  U* xsp = (U*)xs.p;
+  if (R <= kSortSmall)
+    return launch_chained(dispatch_small_kernel<U>, dim3(R + 1), dim3(256), 0, stream, idx, R, k, E, perm, inv, offsets,
+                          xp, ldx, xsp, ldxs, n);
+  int32_t* hist = (int32_t*)ws;
+  const int per = sort_per_block(R), nblk = (R + per - 1) / per;
+  cudaError_t e = launch_chained(sort_hist_kernel, dim3(nblk), dim3(kSortBlock), 0, stream, idx, R, per, E, hist);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(sort_rank_kernel, dim3(nblk), dim3(kSortBlock), (size_t)32 * (E + 1), stream, idx, R, per, E,
+                     (const int32_t*)hist, perm, inv, offsets);
+  if (e != cudaSuccess || !xp) return e;
+  const int threads = n >= 256 ? 256 : (n + 31) / 32 * 32;
+  return launch_chained(dispatch_rows_kernel<U>, dim3(T), dim3(threads), 0, stream, xp, ldx, (const int32_t*)inv, k,
+                        xsp, ldxs, n);
+}
+
+template <typename T, int N>
+cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y,
+                       cudaStream_t stream) {
+  const int cols = (H + N - 1) / N;
+  const int threads = cols >= 256 ? 256 : (cols + 31) / 32 * 32;
+  int ny = 1;  // column blocks: more parallelism for few tokens
+  while (T_ * ny < 592 && ny * threads < cols) ny *= 2;
+  return launch_chained(collect_rows_kernel<T, N>, dim3(T_, ny), dim3(threads), 0, stream, (const T*)o.p, o.ld, w, inv,
+                        T_ * k, k, H, (T*)y.p, y.ld);
+}
+
+template <typename T, int N>
+cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
+                                Rows d_o, float* dw, cudaStream_t stream) {
+  const int cols = (H + N - 1) / N;
+  const int most = T_ >= 592 ? 256 : 512;
+  const int threads = cols >= most ? most : (cols + 31) / 32 * 32;
+  return launch_chained(collect_backward_kernel<T, N>, dim3(T_), dim3(threads), 0, stream, (const T*)dy.p, dy.ld,
+                        (const T*)o.p, o.ld, w, inv, T_ * k, k, H, (T*)d_o.p, d_o.ld, dw);
+}
+
+bool rows16(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 16 == 0; }
+
+}  // namespace
+
+uint64_t sort_ws_bytes(int R, int E) {
+  if (R <= kSortSmall) return 256;
+  const int per = sort_per_block(R);
+  return up256((uint64_t)((R + per - 1) / per) * (E + 1) * 4);
+}
+
+cudaError_t launch_dispatch(const int32_t* idx, int T, int k, int E, int32_t* perm, int32_t* inv, int32_t* offsets,
+                            ConstRows x, Rows xs, int H, int dtype, void* ws, cudaStream_t stream) {
+  const int es = dtype_size(dtype);
+  const uint64_t all = (uintptr_t)x.p | (uintptr_t)xs.p | (uint64_t)(x.ld * es) | (uint64_t)(xs.ld * es) |
+                       (uint64_t)((int64_t)H * es);
+  if ((all & 15) == 0) return dispatch_as<uint4>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
+  if ((all & 3) == 0) return dispatch_as<uint32_t>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
+  return dispatch_as<uint16_t>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
+}
+
+cudaError_t launch_collect(ConstRows o, const float* w, const int32_t* inv, int T, int k, int H, int dtype, Rows y,
+                           cudaStream_t stream) {
+  const int es = dtype_size(dtype);
+  const bool vec = rows16(o.p, o.ld, es) && rows16(y.p, y.ld, es) && ((int64_t)H * es) % 16 == 0;
+  if (dtype == MOE_F32)
+    return vec ? collect_as<float, 4>(o, w, inv, T, k, H, y, stream) : collect_as<float, 1>(o, w, inv, T, k, H, y, stream);
+  if (dtype == MOE_F16)
+    return vec ? collect_as<__half, 8>(o, w, inv, T, k, H, y, stream)
+               : collect_as<__half, 1>(o, w, inv, T, k, H, y, stream);
+  return vec ? collect_as<__nv_bfloat16, 8>(o, w, inv, T, k, H, y, stream)
+             : collect_as<__nv_bfloat16, 1>(o, w, inv, T, k, H, y, stream);
+}
+
+cudaError_t launch_collect_backward(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T, int k, int H,
+                                    int dtype, Rows d_o, float* dw, cudaStream_t stream) {
+  const int es = dtype_size(dtype);
+  const bool vec = rows16(dy.p, dy.ld, es) && rows16(o.p, o.ld, es) && rows16(d_o.p, d_o.ld, es) &&
+                   ((int64_t)H * es) % 16 == 0;
+  if (dtype == MOE_F32)
+    return vec ? collect_backward_as<float, 4>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+               : collect_backward_as<float, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+  if (dtype == MOE_F16)
+    return vec ? collect_backward_as<__half, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+               : collect_backward_as<__half, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+  return vec ? collect_backward_as<__nv_bfloat16, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+             : collect_backward_as<__nv_bfloat16, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+}
+
+}  // namespace moe
