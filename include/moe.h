@@ -375,8 +375,9 @@ enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
  * inv: DEVICE i32 [T*k]; inv[entry] = row, -1 for a dropped entry.
  * offsets: DEVICE i32 [E+1]; group e has rows [offsets[e], offsets[e+1]);
  *   offsets[E] = rows that have a group.
- * ws: DEVICE, 256-byte aligned; ws == NULL -> *ws_bytes_out = the size needed
- *   for (T, k, E) and nothing runs.
+ * ws: DEVICE, 256-byte aligned; ws == NULL with ws_bytes_out -> *ws_bytes_out = the
+ *   size needed for (T, k, E) and nothing runs.  T*k <= 1024 needs none (size 0):
+ *   ws and ws_bytes_out may both be NULL then.
  * Limits: 1 <= k <= 8, T*k <= 2^20, 1 <= E <= MOE_MAX_GROUPS.
  * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_SHAPE, MOE_ERR_WORKSPACE,
  *   MOE_ERR_UNSUPPORTED_DEVICE, MOE_ERR_CUDA (those of every operator below too).
@@ -475,7 +476,8 @@ MOE_API moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t dty
  * Limits: T <= 2^20; 1 <= n <= MOE_MAX_GROUPS; r a multiple of 8 up to 128; K and N
  *   multiples of 8 from 8 to 2^20.  All matrices 16-byte aligned, pitches multiples of
  *   8 values (MOE_ERR_ALIGN).
- * ws as for moe_sort; its size depends on (T, K, r, n).
+ * ws: DEVICE, 256-byte aligned; ws == NULL -> *ws_bytes_out = the size needed for
+ *   (T, K, r, n) and nothing runs.
  */
 MOE_API moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
                                 int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,

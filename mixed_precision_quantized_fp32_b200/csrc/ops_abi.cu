@@ -22,7 +22,7 @@ moe_status sort_rows(const void* x, int64_t ldx, int32_t dtype, const int32_t* i
                      uint64_t* ws_bytes_out, cudaStream_t stream) {
   const uint64_t need = sort_ws_bytes(T * k, E);
   if (ws_bytes_out) *ws_bytes_out = need;
-  if (!ws) return ws_bytes_out ? MOE_OK : MOE_ERR_ARG;
+  if (!ws && (ws_bytes_out || need > 0)) return ws_bytes_out ? MOE_OK : MOE_ERR_ARG;
   if (!offsets || (T > 0 && (!idx || !perm || !inv))) return MOE_ERR_ARG;
   if (!on(idx, 4) || !on(perm, 4) || !on(inv, 4) || !on(offsets, 4) || !on(ws, 256)) return MOE_ERR_ALIGN;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -50,7 +50,7 @@ extern "C" moe_status moe_dispatch(const void* x, int64_t ldx, int32_t dtype, co
                                    cudaStream_t stream) {
   if (!entries_ok(T, k) || E < 1 || E > kMaxGroups || !width_ok(H)) return MOE_ERR_SHAPE;
   if (!known_type(dtype)) return MOE_ERR_FORMAT;
-  if (ws) {
+  if (ws || !ws_bytes_out) {  // not a size query
     const int es = dtype_size(dtype);
     if (T > 0 && (!x || !xs)) return MOE_ERR_ARG;
     if (ldx < H || ldxs < H) return MOE_ERR_SHAPE;

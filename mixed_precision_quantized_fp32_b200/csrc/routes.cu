@@ -330,7 +330,7 @@ bool rows16(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 1
 }  // namespace
 
 uint64_t sort_ws_bytes(int R, int E) {
-  if (R <= kSortSmall) return 256;
+  if (R <= kSortSmall) return 0;
   const int per = sort_per_block(R);
   return up256((uint64_t)((R + per - 1) / per) * (E + 1) * 4);
 }

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -23,44 +24,45 @@ _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 GROUP = 32  # columns of an 8-bit checkpoint that share a scale
 
 
+# The current device and stream as plain numbers: torch.cuda.current_stream() builds an
+# object, 2 us of the 6 to 10 that a call takes on the host.
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _Call:
     """Device and stream of one call, taken from its first tensor."""
 
-    __slots__ = ("device", "stream", "raw", "other")
+    __slots__ = ("dev", "stream")
 
     def __init__(self, t: torch.Tensor, stream: torch.cuda.Stream | None):
-        if not t.is_cuda:
-            raise ValueError("operands must be cuda tensors")
-        self.device = t.device
-        self.other = torch.cuda.current_device() != t.device.index
+        self.dev = t.get_device()
         self.stream = stream
-        if stream is not None and stream.device != t.device:
+        if self.dev < 0:
+            raise ValueError("operands must be cuda tensors")
+        if stream is not None and stream.device_index != self.dev:
             raise ValueError(f"the stream is on {stream.device}, the operands on {t.device}")
-        self.raw = (stream or torch.cuda.current_stream(t.device)).cuda_stream
 
-    def empty(self, shape, dtype) -> torch.Tensor:
+    def empty(self, like: torch.Tensor, shape, dtype) -> torch.Tensor:
         # on the stream of the call, so that the allocator does not hand the memory on early
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
 
     def run(self, fn, *args) -> None:
-        if self.other:
-            with torch.cuda.device(self.device):
-                check(fn.__name__, fn(*args, self.raw))
+        if _device() != self.dev:
+            with torch.cuda.device(self.dev):
+                rc = fn(*args, self.stream.cuda_stream if self.stream is not None else _raw_stream(self.dev))
         else:
-            check(fn.__name__, fn(*args, self.raw))
-
-    def workspace(self, fn, *args) -> torch.Tensor:
-        need = C.c_uint64(0)
-        check(f"{fn.__name__}(workspace query)", fn(*args, C.byref(need), None))
-        return self.empty((need.value,), torch.uint8)
+            rc = fn(*args, self.stream.cuda_stream if self.stream is not None else _raw_stream(self.dev))
+        if rc:
+            check(fn.__name__, rc)
 
     def rows(self, t: torch.Tensor, name: str, R: int, F: int, dtype) -> tuple[int, int]:
         """Pointer and pitch of a matrix [R, F] with contiguous rows."""
-        if t.dtype is not dtype or t.device != self.device or t.shape != (R, F):
-            raise ValueError(f"{name} must be a {dtype} tensor {[R, F]} on {self.device}, got {t.dtype} "
+        if t.dtype is not dtype or t.get_device() != self.dev or t.shape != (R, F):
+            raise ValueError(f"{name} must be a {dtype} tensor {[R, F]} on cuda:{self.dev}, got {t.dtype} "
                              f"{list(t.shape)} on {t.device}")
         ld, step = t.stride()
         if step != 1 and F > 1:
@@ -68,10 +70,20 @@ class _Call:
         return t.data_ptr(), (ld if R > 1 else F)
 
     def flat(self, t: torch.Tensor, name: str, count: int, dtype) -> int:
-        if t.dtype is not dtype or t.device != self.device or t.numel() != count or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} values on {self.device}, got "
+        if t.dtype is not dtype or t.get_device() != self.dev or t.numel() != count or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} values on cuda:{self.dev}, got "
                              f"{t.dtype} {list(t.shape)} on {t.device}")
         return t.data_ptr()
+
+    def memory(self, ws: torch.Tensor | None, like: torch.Tensor, need: int) -> tuple[torch.Tensor | None, int | None, int]:
+        """A workspace of at least `need` bytes: (tensor, pointer, bytes)."""
+        if ws is None:
+            if need == 0:
+                return None, None, 0
+            ws = self.empty(like, (need,), torch.uint8)
+        elif ws.get_device() != self.dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous memory on cuda:{self.dev}")
+        return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _values(t: torch.Tensor, name: str) -> torch.dtype:
@@ -106,10 +118,18 @@ def _routes(c: _Call, r: Routes) -> tuple[int, int, int]:
             c.flat(r.offsets, "offsets", r.E + 1, torch.int32))
 
 
-def _new_routes(c: _Call, T: int, k: int, E: int, routes: Routes | None) -> Routes:
+@lru_cache(maxsize=4096)
+def sort_workspace_bytes(T: int, k: int, E: int) -> int:
+    """Bytes of ws that moe_sort and moe_dispatch need (0: none)."""
+    need = C.c_uint64(0)
+    check("moe_sort(workspace query)", _lib.load().moe_sort(None, T, k, E, None, None, None, None, 0, C.byref(need), None))
+    return need.value
+
+
+def _new_routes(c: _Call, idx: torch.Tensor, T: int, k: int, E: int, routes: Routes | None) -> Routes:
     if routes is None:
         R = T * k
-        buf = c.empty((2 * R + max(E, 0) + 1,), torch.int32)
+        buf = c.empty(idx, (2 * R + max(E, 0) + 1,), torch.int32)
         return Routes(T, k, E, buf[:R], buf[R:2 * R], buf[2 * R:])
     if (routes.T, routes.k, routes.E) != (T, k, E):
         raise ValueError(f"routes are for {(routes.T, routes.k, routes.E)} tokens, entries and groups, need {(T, k, E)}")
@@ -129,12 +149,10 @@ def moe_sort(idx: torch.Tensor, E: int, routes: Routes | None = None, ws: torch.
     c = _Call(idx, stream)
     T, k = _index(idx)
     ip = c.flat(idx, "idx", T * k, torch.int32)
-    routes = _new_routes(c, T, k, E, routes)
+    routes = _new_routes(c, idx, T, k, E, routes)
     r = _routes(c, routes)
-    fn = _lib.load().moe_sort
-    if ws is None:
-        ws = c.workspace(fn, None, T, k, E, None, None, None, None, 0)
-    c.run(fn, ip, T, k, E, *r, ws.data_ptr(), ws.numel(), None)
+    ws, wp, wn = c.memory(ws, idx, sort_workspace_bytes(T, k, E))
+    c.run(_lib.load().moe_sort, ip, T, k, E, *r, wp, wn, None)
     return routes
 
 
@@ -149,15 +167,13 @@ def moe_dispatch(x: torch.Tensor, idx: torch.Tensor, E: int, xs: torch.Tensor | 
     H = x.shape[1]
     xp, ldx = c.rows(x, "x", T, H, dt)
     ip = c.flat(idx, "idx", T * k, torch.int32)
-    routes = _new_routes(c, T, k, E, routes)
+    routes = _new_routes(c, idx, T, k, E, routes)
     r = _routes(c, routes)
     if xs is None:
-        xs = c.empty((T * k, H), dt)
+        xs = c.empty(x, (T * k, H), dt)
     xsp, ldxs = c.rows(xs, "xs", T * k, H, dt)
-    fn = _lib.load().moe_dispatch
-    if ws is None:
-        ws = c.workspace(fn, None, ldx, _DTYPE[dt], None, T, k, E, H, None, ldxs, None, None, None, None, 0)
-    c.run(fn, xp, ldx, _DTYPE[dt], ip, T, k, E, H, xsp, ldxs, *r, ws.data_ptr(), ws.numel(), None)
+    ws, wp, wn = c.memory(ws, idx, sort_workspace_bytes(T, k, E))
+    c.run(_lib.load().moe_dispatch, xp, ldx, _DTYPE[dt], ip, T, k, E, H, xsp, ldxs, *r, wp, wn, None)
     return xs, routes
 
 
@@ -169,7 +185,7 @@ def moe_dispatch_backward(dxs: torch.Tensor, routes: Routes, dx: torch.Tensor | 
     T, k, H = routes.T, routes.k, dxs.shape[1]
     dp, ldd = c.rows(dxs, "dxs", T * k, H, dt)
     if dx is None:
-        dx = c.empty((T, H), dt)
+        dx = c.empty(dxs, (T, H), dt)
     xp, ldx = c.rows(dx, "dx", T, H, dt)
     c.run(_lib.load().moe_dispatch_backward, dp, ldd, _DTYPE[dt], c.flat(routes.inv, "inv", T * k, torch.int32), T, k, H,
           xp, ldx)
@@ -184,7 +200,7 @@ def moe_collect(o: torch.Tensor, w: torch.Tensor, routes: Routes, y: torch.Tenso
     T, k, H = routes.T, routes.k, o.shape[1]
     op, ldo = c.rows(o, "o", T * k, H, dt)
     if y is None:
-        y = c.empty((T, H), dt)
+        y = c.empty(o, (T, H), dt)
     yp, ldy = c.rows(y, "y", T, H, dt)
     c.run(_lib.load().moe_collect, op, ldo, _DTYPE[dt], c.flat(w, "w", T * k, torch.float32),
           c.flat(routes.inv, "inv", T * k, torch.int32), T, k, H, yp, ldy)
@@ -202,9 +218,9 @@ def moe_collect_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Tensor, rou
     gp, ldg = c.rows(dy, "dy", T, H, dt)
     op, ldo = c.rows(o, "o", T * k, H, dt)
     if do is None:
-        do = c.empty((T * k, H), dt)
+        do = c.empty(o, (T * k, H), dt)
     if dw is None:
-        dw = c.empty((T, k), torch.float32)
+        dw = c.empty(w, (T, k), torch.float32)
     dp, ldd = c.rows(do, "do", T * k, H, dt)
     c.run(_lib.load().moe_collect_backward, gp, ldg, op, ldo, _DTYPE[dt], c.flat(w, "w", T * k, torch.float32),
           c.flat(routes.inv, "inv", T * k, torch.int32), T, k, H, dp, ldd, c.flat(dw, "dw", T * k, torch.float32))
@@ -212,13 +228,50 @@ def moe_collect_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Tensor, rou
 
 
 # ------------------------------------------------------------------ 8-bit checkpoints
-@dataclass
 class ActCkpt:
-    """A matrix of activations in 8 bits: values codes * 2**(exps - 127), one exponent per
-    row and 32 columns (255: the group held an infinity or a NaN)."""
-    codes: torch.Tensor  # int8 [R, F]
-    exps: torch.Tensor   # uint8 [R, ceil(F/32)]
-    dtype: torch.dtype   # type of the saved values
+    """A matrix [R, F] of activations in 8 bits: values codes * 2**(exps - 127), one exponent
+    per row and 32 columns (255: the group held an infinity or a NaN).
+
+    codes: int8 [R, F]; exps: uint8 [R, ceil(F/32)]; dtype: type of the saved values.
+    A checkpoint that an operator allocates is one piece of memory, of which codes and exps
+    are views."""
+
+    __slots__ = ("R", "F", "dtype", "_codes", "_exps", "_mem", "_at")
+
+    def __init__(self, codes: torch.Tensor, exps: torch.Tensor, dtype: torch.dtype):
+        if codes.dim() != 2 or codes.dtype is not torch.int8 or not codes.is_contiguous():
+            raise ValueError(f"codes must be a contiguous int8 matrix, got {codes.dtype} {list(codes.shape)}")
+        self.R, self.F = codes.shape
+        if tuple(exps.shape) != (self.R, -(-self.F // GROUP)) or exps.dtype is not torch.uint8 \
+                or not exps.is_contiguous() or exps.device != codes.device:
+            raise ValueError(f"exps must be a contiguous uint8 tensor {[self.R, -(-self.F // GROUP)]} on {codes.device}, "
+                             f"got {exps.dtype} {list(exps.shape)} on {exps.device}")
+        self.dtype, self._codes, self._exps, self._mem, self._at = dtype, codes, exps, None, 0
+
+    @staticmethod
+    def _bytes(R: int, F: int) -> tuple[int, int]:
+        """Offset of the exponents behind the codes, and the whole size (both whole 256s)."""
+        e = (R * F + 255) // 256 * 256
+        return e, e + (R * -(-F // GROUP) + 255) // 256 * 256
+
+    @classmethod
+    def _in(cls, mem: torch.Tensor, at: int, R: int, F: int, dtype: torch.dtype) -> "ActCkpt":
+        k = cls.__new__(cls)
+        k.R, k.F, k.dtype, k._codes, k._exps, k._mem, k._at = R, F, dtype, None, None, mem, at
+        return k
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._mem[self._at:self._at + self.R * self.F].view(torch.int8).view(self.R, self.F)
+        return self._codes
+
+    @property
+    def exps(self) -> torch.Tensor:
+        if self._exps is None:
+            at, G = self._at + self._bytes(self.R, self.F)[0], -(-self.F // GROUP)
+            self._exps = self._mem[at:at + self.R * G].view(self.R, G)
+        return self._exps
 
 
 @dataclass
@@ -228,17 +281,25 @@ class SwigluCkpt:
 
 
 def alloc_ckpt(R: int, F: int, dtype: torch.dtype, device=None) -> ActCkpt:
-    d = device or "cuda"
-    return ActCkpt(torch.empty((R, F), dtype=torch.int8, device=d),
-                   torch.empty((R, -(-F // GROUP)), dtype=torch.uint8, device=d), dtype)
+    """Memory for the 8-bit checkpoint of a matrix [R, F] of dtype."""
+    return ActCkpt._in(torch.empty(ActCkpt._bytes(R, F)[1], dtype=torch.uint8, device=device or "cuda"), 0, R, F, dtype)
 
 
 def _ckpt(c: _Call, k: ActCkpt, R: int, F: int) -> tuple[int, int]:
-    return c.flat(k.codes, "codes", R * F, torch.int8), c.flat(k.exps, "exps", R * -(-F // GROUP), torch.uint8)
+    """Pointers of a checkpoint's codes and exponents."""
+    mem = k._codes if k._mem is None else k._mem
+    if k.R != R or k.F != F or mem.get_device() != c.dev:
+        raise ValueError(f"the checkpoint must be of {[R, F]} on cuda:{c.dev}, is of {[k.R, k.F]} on {mem.device}")
+    if k._mem is None:
+        return k._codes.data_ptr(), k._exps.data_ptr()
+    p = k._mem.data_ptr() + k._at
+    return p, p + k._bytes(R, F)[0]
 
 
-def _new_ckpt(c: _Call, R: int, F: int, dt) -> ActCkpt:
-    return ActCkpt(c.empty((R, F), torch.int8), c.empty((R, -(-F // GROUP)), torch.uint8), dt)
+def _new_ckpts(c: _Call, like: torch.Tensor, R: int, F: int, dt, count: int) -> list[ActCkpt]:
+    size = ActCkpt._bytes(R, F)[1]
+    mem = c.empty(like, (count * size,), torch.uint8)
+    return [ActCkpt._in(mem, i * size, R, F, dt) for i in range(count)]
 
 
 def _limit(c: _Call, rows: torch.Tensor | None) -> int | None:
@@ -254,7 +315,7 @@ def moe_act_save(x: torch.Tensor, ckpt: ActCkpt | None = None, rows: torch.Tenso
     R, F = x.shape
     xp, ldx = c.rows(x, "x", R, F, dt)
     if ckpt is None:
-        ckpt = _new_ckpt(c, R, F, dt)
+        ckpt, = _new_ckpts(c, x, R, F, dt, 1)
     elif ckpt.dtype is not dt:
         raise ValueError(f"the checkpoint is for {ckpt.dtype}, x is {dt}")
     c.run(_lib.load().moe_act_save, xp, ldx, _DTYPE[dt], R, F, *_ckpt(c, ckpt, R, F), _limit(c, rows))
@@ -264,12 +325,11 @@ def moe_act_save(x: torch.Tensor, ckpt: ActCkpt | None = None, rows: torch.Tenso
 def moe_act_load(ckpt: ActCkpt, x: torch.Tensor | None = None, rows: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The restored matrix, in the type that was saved or in that of x."""
-    c = _Call(ckpt.codes, stream)
-    if ckpt.codes.dim() != 2:
-        raise ValueError(f"codes must be a matrix, got {list(ckpt.codes.shape)}")
-    R, F = ckpt.codes.shape
+    mem = ckpt._codes if ckpt._mem is None else ckpt._mem
+    c = _Call(mem, stream)
+    R, F = ckpt.R, ckpt.F
     if x is None:
-        x = c.empty((R, F), ckpt.dtype)
+        x = c.empty(mem, (R, F), ckpt.dtype)
     dt = _values(x, "x")
     xp, ldx = c.rows(x, "x", R, F, dt)
     c.run(_lib.load().moe_act_load, *_ckpt(c, ckpt, R, F), R, F, _DTYPE[dt], xp, ldx, _limit(c, rows))
@@ -286,10 +346,10 @@ def moe_swiglu_save(g: torch.Tensor, u: torch.Tensor, h: torch.Tensor | None = N
     gp, ldg = c.rows(g, "g", R, F, dt)
     up, ldu = c.rows(u, "u", R, F, dt)
     if h is None:
-        h = c.empty((R, F), dt)
+        h = c.empty(g, (R, F), dt)
     hp, ldh = c.rows(h, "h", R, F, dt)
     if ckpt is None:
-        ckpt = SwigluCkpt(_new_ckpt(c, R, F, dt), _new_ckpt(c, R, F, dt))
+        ckpt = SwigluCkpt(*_new_ckpts(c, g, R, F, dt, 2))
     elif ckpt.g.dtype is not dt or ckpt.u.dtype is not dt:
         raise ValueError(f"the checkpoint is for {ckpt.g.dtype} and {ckpt.u.dtype}, g is {dt}")
     c.run(_lib.load().moe_swiglu_save, gp, ldg, up, ldu, _DTYPE[dt], R, F, hp, ldh, *_ckpt(c, ckpt.g, R, F),
@@ -308,11 +368,11 @@ def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | N
     R, F = dh.shape
     ap, lda = c.rows(dh, "dh", R, F, dt)
     if dg is None:
-        dg = c.empty((R, F), dt)
+        dg = c.empty(dh, (R, F), dt)
     if du is None:
-        du = c.empty((R, F), dt)
+        du = c.empty(dh, (R, F), dt)
     if h is None and rebuild_h:
-        h = c.empty((R, F), dt)
+        h = c.empty(dh, (R, F), dt)
     gp, ldg = c.rows(dg, "dg", R, F, dt)
     up, ldu = c.rows(du, "du", R, F, dt)
     hp, ldh = (None, F) if h is None else c.rows(h, "h", R, F, dt)
@@ -322,6 +382,15 @@ def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | N
 
 
 # ------------------------------------------------------------------ adapters
+@lru_cache(maxsize=4096)
+def adapters_workspace_bytes(T: int, K: int, N: int, r: int, n: int) -> int:
+    """Bytes of ws that moe_adapters needs."""
+    need = C.c_uint64(0)
+    check("moe_adapters(workspace query)", _lib.load().moe_adapters(
+        None, K, None, N, 0, T, K, N, r, n, None, None, None, None, None, None, N, None, 0, C.byref(need), None))
+    return need.value
+
+
 def moe_adapters(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
                  routes: Routes, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
@@ -346,16 +415,13 @@ def moe_adapters(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Ten
     sp = c.flat(scale, "scale", n, torch.float32)
     pp, _, fp = _routes(c, routes)
     if out is None:
-        out = c.empty((T, N), dt)
+        out = c.empty(y, (T, N), dt)
     op, ldo = c.rows(out, "out", T, N, dt)
-    fn = _lib.load().moe_adapters
-    if ws is None:
-        ws = c.workspace(fn, None, ldx, None, ldy, _DTYPE[dt], T, K, N, r, n, None, None, None, None, None, None, ldo,
-                         None, 0)
-    c.run(fn, xp, ldx, yp, ldy, _DTYPE[dt], T, K, N, r, n, ap, bp, sp, pp, fp, op, ldo, ws.data_ptr(), ws.numel(), None)
+    ws, wp, wn = c.memory(ws, x, adapters_workspace_bytes(T, K, N, r, n))
+    c.run(_lib.load().moe_adapters, xp, ldx, yp, ldy, _DTYPE[dt], T, K, N, r, n, ap, bp, sp, pp, fp, op, ldo, wp, wn, None)
     return out
 
 
-__all__ = ["ActCkpt", "Routes", "SwigluCkpt", "alloc_ckpt", "alloc_routes", "moe_act_load", "moe_act_save",
-           "moe_adapters", "moe_collect", "moe_collect_backward", "moe_dispatch", "moe_dispatch_backward", "moe_sort",
-           "moe_swiglu_backward", "moe_swiglu_save"]
+__all__ = ["ActCkpt", "Routes", "SwigluCkpt", "adapters_workspace_bytes", "alloc_ckpt", "alloc_routes", "moe_act_load",
+           "moe_act_save", "moe_adapters", "moe_collect", "moe_collect_backward", "moe_dispatch", "moe_dispatch_backward",
+           "moe_sort", "moe_swiglu_backward", "moe_swiglu_save", "sort_workspace_bytes"]
