@@ -476,13 +476,11 @@ MOE_API moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t dty
  * Limits: T <= 2^20; 1 <= n <= MOE_MAX_GROUPS; r a multiple of 8 up to 128; K and N
  *   multiples of 8 from 8 to 2^20.  All matrices 16-byte aligned, pitches multiples of
  *   8 values (MOE_ERR_ALIGN).
- * ws: DEVICE, 256-byte aligned; ws == NULL -> *ws_bytes_out = the size needed for
- *   (T, K, r, n) and nothing runs.
  */
 MOE_API moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
                                 int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
                                 const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
-                                int64_t ldo, void* ws, uint64_t ws_bytes, uint64_t* ws_bytes_out, cudaStream_t stream);
+                                int64_t ldo, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

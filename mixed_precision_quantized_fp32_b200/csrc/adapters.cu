@@ -3,17 +3,19 @@
 // out[t] = y[t] for a token without one.
 //
 // Tokens come sorted by adapter (routes.cu), so a tile of rows shares its adapter and
-// both products are matrix products of a tile of tokens with A_a and B_a:
-//   adapter_down_kernel   P[row][r] = sum_k x[k] A_a[r][k], split over k where there are
-//                         few tiles; each part is written in fp32 and nothing is added
-//                         in memory
-//   adapter_up_kernel     sums the parts in order, scales, multiplies by B_a and adds y
+// both products are matrix products of a tile of tokens with A_a and B_a.  A cluster of
+// 1 to 8 blocks takes one tile: each block has a share of the k values for
+//   P[row][r] = sum_k x[k] A_a[r][k]
+// in fp32, the blocks read one another's shares from distributed shared memory and add
+// them in order, and each block then has a share of the outputs for scale * P B_a^T + y.
+// One launch, no workspace, nothing added in global memory.
+//
 // Arithmetic per byte is about the rank, far below what the tensor cores need to be the
-// bound, so the operands go from memory straight to mma.sync fragments: the contraction
+// bound, so operands go from memory straight to mma.sync fragments: the contraction
 // index may be permuted if both operands are permuted alike, and with a lane taking
 // eight consecutive values (16 bytes) of its row as its share of 32, every load is a
-// full 16 bytes and no shared memory is staged.  The up product's fp32 operand P goes
-// in as two terms of the value type (P = hi + lo, 16 or more bits), so its rounding
+// full 16 bytes and nothing is staged in shared memory.  The up product's fp32 operand P
+// goes in as two terms of the value type (P = hi + lo, 16 or more bits), so its rounding
 // stays far below that of the stored result; in fp16 a row is first brought to at most
 // 2^14 by a power of two, since P may pass fp16's range.
 #include "ops_common.cuh"
@@ -22,7 +24,7 @@ namespace moe {
 
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = 32 * kAdWarps;
-constexpr int kAdStep = 32 * kAdWarps;  // k values a block takes at once
+constexpr int kAdMaxCluster = 8;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -94,98 +96,6 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
   return found;
 }
 
-// NR: n8 tiles of the rank (r <= 8*NR), MT: m16 tiles of tokens.
-template <typename T, int NR, int MT>
-__global__ void __launch_bounds__(kAdThreads) adapter_down_kernel(const T* __restrict__ x, int64_t ldx, int T_, int K,
-                                                                  int r, int n, const T* __restrict__ A,
-                                                                  const int32_t* __restrict__ perm,
-                                                                  const int32_t* __restrict__ offsets, int kslice,
-                                                                  float* __restrict__ part) {
-  pdl_enter();  // before any global memory access (see moe_common.cuh)
-  constexpr int TM = 16 * MT;
-  __shared__ float red[kAdWarps / 2][TM * NR * 8];
-  const Tile tile = find_tile(blockIdx.x, TM, offsets, n, T_, false);
-  if (tile.rows == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const T* xr[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * m + 8 * h + g;
-      const int t = i < tile.rows ? perm[tile.row0 + i] : -1;
-      xr[m][h] = (unsigned)t < (unsigned)T_ ? x + (int64_t)t * ldx : nullptr;
-    }
-  const T* Ar = A + ((int64_t)tile.adapter * r + g) * K;
-  float acc[MT][NR][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.0f;
-  const int k0 = blockIdx.y * kslice, k1 = min(K, k0 + kslice);
-#pragma unroll 2
-  for (int kk = k0 + warp * 32 + q * 8; kk - q * 8 < k1; kk += kAdStep) {
-    const bool in = kk < k1;  // K is a multiple of 8
-    uint4 av[MT][2], bv[NR];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        av[m][h] = in && xr[m][h] ? __ldg(reinterpret_cast<const uint4*>(xr[m][h] + kk)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      bv[i] = in && 8 * i < r ? __ldg(reinterpret_cast<const uint4*>(Ar + (int64_t)8 * i * K + kk))
-                              : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const uint32_t a0[4] = {av[m][0].x, av[m][1].x, av[m][0].y, av[m][1].y};
-      const uint32_t a1[4] = {av[m][0].z, av[m][1].z, av[m][0].w, av[m][1].w};
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        mma16816<T>(acc[m][i], a0, bv[i].x, bv[i].y);
-        mma16816<T>(acc[m][i], a1, bv[i].z, bv[i].w);
-      }
-    }
-  }
-  // sum over the warps: upper half to shared memory, lower half adds, three times
-#pragma unroll
-  for (int half = kAdWarps / 2; half > 0; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) red[warp - half][((m * NR + i) * 4 + c) * 32 + lane] = acc[m][i][c];
-    }
-    __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][i][c] += red[warp][((m * NR + i) * 4 + c) * 32 + lane];
-    }
-    __syncthreads();
-  }
-  if (warp == 0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * m + 8 * h + g;
-        if (row >= tile.rows) continue;
-        float* out = part + ((int64_t)blockIdx.y * T_ + tile.row0 + row) * r + 2 * q;
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-          if (8 * i < r) *reinterpret_cast<float2*>(out + 8 * i) = make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
-      }
-  }
-}
-
 // Two values as hi and lo terms of T; an infinity stays one (inf - inf would be NaN).
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -194,91 +104,169 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// A float of block `rank`'s shared memory at the place that p has in this block's.
+__device__ __forceinline__ float load_remote(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+
+// NR: n8 tiles of the rank (r <= 8*NR).  MT: m16 tiles of tokens; the 8 warps are MT token
+// tiles times 8/MT shares of k, then of the outputs.
 template <typename T, int NR, int MT>
-__global__ void __launch_bounds__(kAdThreads) adapter_up_kernel(const T* y, int64_t ldy, int T_, int N,
-                                                                int r, int n, const T* __restrict__ B,
-                                                                const float* __restrict__ scale,
-                                                                const int32_t* __restrict__ perm,
-                                                                const int32_t* __restrict__ offsets, bool rest,
-                                                                int parts, const float* __restrict__ part,
-                                                                int nslice, T* out, int64_t ldo) {
+__global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
+    adapter_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r, int n,
+                   const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
+                   const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
+                   int kslice, int nslice, T* out, int64_t ldo) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  constexpr int TM = 16 * MT, KB = (NR + 3) / 4, LD = KB * 32 + 4;
-  __shared__ float P[TM][LD];
-  __shared__ float undo[TM];
-  const Tile tile = find_tile(blockIdx.x, TM, offsets, n, T_, rest);
-  if (tile.rows == 0) return;
+  constexpr int TM = 16 * MT, KG = kAdWarps / MT, KB = (NR + 3) / 4, RP = KB * 32, LD = RP + 4;
+  extern __shared__ float sm[];
+  float* red = sm;                            // [KG][TM][NR*8] shares of the warps
+  float* mine = red + KG * TM * NR * 8;       // [TM][NR*8] this block's share of P
+  float* P = mine + TM * NR * 8;              // [TM][LD]
+  float* undo = P + TM * LD;                  // [TM] fp16: what takes a row's power of two back
+  const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, rest);
+  if (tile.rows == 0) return;  // all blocks of the cluster alike
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int m = warp % MT, part = warp / MT;
   const bool has = tile.adapter < n;
-  const T* yr[MT][2];
-  T* orow[MT][2];
+  const int n0 = rank * nslice, n1 = min(N, n0 + nslice);
+  int tok[2];  // tokens of the lane's rows, -1: none
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * m + 8 * h + g;
-      const int t = i < tile.rows ? perm[tile.row0 + i] : -1;
-      const bool ok = (unsigned)t < (unsigned)T_;
-      yr[m][h] = ok ? y + (int64_t)t * ldy : nullptr;
-      orow[m][h] = ok ? out + (int64_t)t * ldo : nullptr;
-    }
-  uint32_t hi[MT][KB][2][4], lo[MT][KB][2][4];
+  for (int h = 0; h < 2; ++h) {
+    const int i = 16 * m + 8 * h + g;
+    const int t = i < tile.rows ? __ldg(perm + tile.row0 + i) : -1;
+    tok[h] = (unsigned)t < (unsigned)T_ ? t : -1;
+  }
+  uint32_t hi[KB][2][4], lo[KB][2][4];
+  const T* Ba = B + (int64_t)(has ? tile.adapter : 0) * N * r;
   if (has) {
-    const float sc = __ldg(scale + tile.adapter);
-    for (int c = threadIdx.x; c < TM * KB * 32; c += kAdThreads) {
-      const int row = c / (KB * 32), i = c % (KB * 32);
-      float s = 0.0f;
-      if (row < tile.rows && i < r)
-        for (int p = 0; p < parts; ++p) s += part[((int64_t)p * T_ + tile.row0 + row) * r + i];
-      P[row][i] = row < tile.rows && i < r ? s * sc : 0.0f;
+    if (MT == 1) {  // few tokens: B's slice is on its way to L2 while A's is multiplied
+      const int64_t bytes = (int64_t)(n1 - n0) * r * sizeof(T);
+      const char* p = reinterpret_cast<const char*>(Ba + (int64_t)n0 * r);
+      for (int64_t c = threadIdx.x * 128; c < bytes; c += kAdThreads * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
     }
+    float acc[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    const T* x0 = x + (int64_t)tok[0] * ldx;
+    const T* x1 = x + (int64_t)tok[1] * ldx;
+    const T* Ar = A + ((int64_t)tile.adapter * r + g) * K;
+    const int k0 = rank * kslice, k1 = min(K, k0 + kslice);
+#pragma unroll 2
+    for (int kk = k0 + part * 32 + q * 8; kk - q * 8 < k1; kk += KG * 32) {
+      const bool in = kk < k1;  // k1 and kk are multiples of 8
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const uint4 a = in && tok[0] >= 0 ? __ldg(reinterpret_cast<const uint4*>(x0 + kk)) : zero;
+      const uint4 b = in && tok[1] >= 0 ? __ldg(reinterpret_cast<const uint4*>(x1 + kk)) : zero;
+      uint4 w[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        w[i] = in && 8 * i < r ? __ldg(reinterpret_cast<const uint4*>(Ar + (int64_t)8 * i * K + kk)) : zero;
+      const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        mma16816<T>(acc[i], a0, w[i].x, w[i].y);
+        mma16816<T>(acc[i], a1, w[i].z, w[i].w);
+      }
+    }
+    // the warps' shares, then the blocks', each added in order
+    float* mr = red + part * TM * NR * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        *reinterpret_cast<float2*>(mr + (16 * m + 8 * h + g) * NR * 8 + 8 * i + 2 * q) =
+            make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
     __syncthreads();
-    if (is_f16<T>) {  // fp16: bring each row to at most 2^14
+    for (int c = threadIdx.x; c < TM * NR * 8; c += kAdThreads) {
+      float s = red[c];
+#pragma unroll
+      for (int p = 1; p < KG; ++p) s += red[p * TM * NR * 8 + c];
+      mine[c] = s;
+    }
+    if (cluster > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    const float sc = __ldg(scale + tile.adapter);
+    for (int c = threadIdx.x; c < TM * RP; c += kAdThreads) {
+      const int row = c / RP, i = c % RP;
+      float s = 0.0f;
+      if (i < r && row < tile.rows) {
+        const float* p = mine + row * NR * 8 + i;
+        if (cluster > 1)
+          for (int b = 0; b < cluster; ++b) s += load_remote(p, b);
+        else
+          s = *p;
+        s *= sc;
+      }
+      P[row * LD + i] = s;
+    }
+    if (cluster > 1) cluster_arrive();  // this block has read; it may not leave before the others have
+    __syncthreads();
+    if constexpr (is_f16<T>) {
       for (int row = warp; row < TM; row += kAdWarps) {
-        uint32_t m = 0;
-        for (int i = lane; i < KB * 32; i += 32) m = max(m, __float_as_uint(P[row][i]) & 0x7FFFFFFFu);
-        m = __reduce_max_sync(0xffffffffu, m);
-        const int e = (int)(m >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-        const bool scaled = m > 0 && m < 0x7F800000u && e > 0;
+        uint32_t big = 0;
+        for (int i = lane; i < RP; i += 32) big = max(big, __float_as_uint(P[row * LD + i]) & 0x7FFFFFFFu);
+        big = __reduce_max_sync(0xffffffffu, big);
+        const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
+        const bool scaled = big < 0x7F800000u && e > 0;
         if (scaled)
-          for (int i = lane; i < KB * 32; i += 32) P[row][i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+          for (int i = lane; i < RP; i += 32) P[row * LD + i] *= __uint_as_float((uint32_t)(127 - e) << 23);
         if (lane == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
       }
       __syncthreads();
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int b = 0; b < KB; ++b)
 #pragma unroll
-      for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float* p = &P[16 * m + 8 * h + g][32 * b + 8 * q];
-          // lane's eight values: pairs 0, 1 to the first MMA, 2, 3 to the second (as B's)
-          split2<T>(p[0], p[1], hi[m][b][0][h], lo[m][b][0][h]);
-          split2<T>(p[2], p[3], hi[m][b][0][2 + h], lo[m][b][0][2 + h]);
-          split2<T>(p[4], p[5], hi[m][b][1][h], lo[m][b][1][h]);
-          split2<T>(p[6], p[7], hi[m][b][1][2 + h], lo[m][b][1][2 + h]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float* p = P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q;
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+        // lane's eight values: pairs 0, 1 to the first MMA, 2, 3 to the second (as B's)
+        split2<T>(u.x, u.y, hi[b][0][h], lo[b][0][h]);
+        split2<T>(u.z, u.w, hi[b][0][2 + h], lo[b][0][2 + h]);
+        split2<T>(v.x, v.y, hi[b][1][h], lo[b][1][h]);
+        split2<T>(v.z, v.w, hi[b][1][2 + h], lo[b][1][2 + h]);
+      }
   }
-  const T* Ba = B + (int64_t)(has ? tile.adapter : 0) * N * r;
-  const int n0 = blockIdx.y * nslice, n1 = min(N, n0 + nslice);
-  for (int nn = n0 + warp * 32; nn < n1; nn += kAdStep) {
+  float back[2] = {1.0f, 1.0f};
+  if constexpr (is_f16<T>) {
+    if (has)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) back[h] = undo[16 * m + 8 * h + g];
+  }
+  for (int nn = n0 + part * 32; nn < n1; nn += KG * 32) {
     // column c of MMA tile i is output nn + 8*(c/2) + 2*i + c%2, so that a lane ends up
     // with outputs nn + 8q .. nn + 8q + 7 of its rows
-    float acc[MT][4][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.0f;
     const int col = nn + 8 * q;
-    uint4 yv[MT][2];
+    uint4 yv[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h)
+      yv[h] = tok[h] >= 0 && col < n1 ? __ldg(reinterpret_cast<const uint4*>(y + (int64_t)tok[h] * ldy + col))
+                                      : make_uint4(0, 0, 0, 0);
+    float acc[4][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        yv[m][h] = yr[m][h] && col < n1 ? __ldg(reinterpret_cast<const uint4*>(yr[m][h] + col)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
     if (has) {
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
@@ -286,101 +274,86 @@ __global__ void __launch_bounds__(kAdThreads) adapter_up_kernel(const T* y, int6
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int o = nn + 8 * (g >> 1) + 2 * i + (g & 1), kk = 32 * b + 8 * q;
-          bv[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk)) : make_uint4(0, 0, 0, 0);
+          bv[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk))
+                                   : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mma16816<T>(acc[m][i], lo[m][b][0], bv[i].x, bv[i].y);
-            mma16816<T>(acc[m][i], lo[m][b][1], bv[i].z, bv[i].w);
-            mma16816<T>(acc[m][i], hi[m][b][0], bv[i].x, bv[i].y);
-            mma16816<T>(acc[m][i], hi[m][b][1], bv[i].z, bv[i].w);
-          }
+        for (int i = 0; i < 4; ++i) {
+          mma16816<T>(acc[i], lo[b][0], bv[i].x, bv[i].y);
+          mma16816<T>(acc[i], lo[b][1], bv[i].z, bv[i].w);
+          mma16816<T>(acc[i], hi[b][0], bv[i].x, bv[i].y);
+          mma16816<T>(acc[i], hi[b][1], bv[i].z, bv[i].w);
+        }
       }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h) {
+      if (tok[h] < 0 || col >= n1) continue;
+      const uint32_t w[4] = {yv[h].x, yv[h].y, yv[h].z, yv[h].w};
+      uint32_t v[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!orow[m][h] || col >= n1) continue;
-        const float s = is_f16<T> && has ? undo[16 * m + 8 * h + g] : 1.0f;
-        const uint32_t w[4] = {yv[m][h].x, yv[m][h].y, yv[m][h].z, yv[m][h].w};
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack2<T>(w[i]);
-          v[i] = has ? pack2<T>(fmaf(s, acc[m][i][2 * h], f.x), fmaf(s, acc[m][i][2 * h + 1], f.y)) : w[i];
-        }
-        *reinterpret_cast<uint4*>(orow[m][h] + col) = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T>(w[i]);
+        v[i] = has ? pack2<T>(fmaf(back[h], acc[i][2 * h], f.x), fmaf(back[h], acc[i][2 * h + 1], f.y)) : w[i];
       }
+      *reinterpret_cast<uint4*>(out + (int64_t)tok[h] * ldo + col) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
   }
+  if (has && cluster > 1) cluster_wait();
 }
 
 // ---------------------------------------------------------------- host
 namespace {
 
-struct AdapterPlan {
-  int nr, mt;      // kernel variant
-  int tiles;       // upper bound on the tiles of adapters
-  int parts, kslice;
-};
-
-// Tiles of 16 tokens for decode batches; for longer ones as many rows as 64 accumulators
-// a lane allow, so that an adapter's matrices are read less often.  Parts of k fill the
-// machine when there are few tiles.
-AdapterPlan adapter_plan(int T, int K, int r, int n) {
-  AdapterPlan p;
-  p.nr = r <= 16 ? 2 : r <= 32 ? 4 : r <= 64 ? 8 : 16;
-  p.mt = T <= 128 ? 1 : p.nr <= 4 ? 4 : 16 / p.nr;
-  const int tm = 16 * p.mt;
-  p.tiles = (T < n ? T : n) + T / tm;
-  if (p.tiles < 1) p.tiles = 1;  // T = 0: sizes only
-  const int steps = (K + kAdStep - 1) / kAdStep;
-  int parts = (4 * 148 + p.tiles - 1) / p.tiles;
-  if (parts > steps) parts = steps;
-  p.kslice = (steps + parts - 1) / parts * kAdStep;
-  p.parts = (K + p.kslice - 1) / p.kslice;
-  return p;
-}
-
 template <typename T, int NR, int MT>
-cudaError_t adapters_as(const AdapterPlan& p, const AdapterArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_chained(adapter_down_kernel<T, NR, MT>, dim3(p.tiles, p.parts), dim3(kAdThreads), 0, stream,
-                                 (const T*)a.x.p, a.x.ld, a.T, a.K, a.r, a.n, (const T*)a.A, a.perm, a.offsets,
-                                 p.kslice, a.part);
-  if (e != cudaSuccess) return e;
+cudaError_t adapters_as(const AdapterArgs& a, cudaStream_t stream) {
+  constexpr int TM = 16 * MT, KG = kAdWarps / MT, KB = (NR + 3) / 4;
+  constexpr int smem = ((KG + 1) * TM * NR * 8 + TM * (KB * 32 + 4) + TM) * (int)sizeof(float);
+  auto kern = adapter_kernel<T, NR, MT>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   const bool rest = a.out.p != a.y.p;  // rows without an adapter still have to be copied
-  const int tiles = p.tiles + (rest ? 1 : 0);  // one more segment of the same T rows
-  const int steps = (a.N + kAdStep - 1) / kAdStep;
-  int slices = (4 * 148 + p.tiles - 1) / p.tiles;
-  if (slices > steps) slices = steps;
-  const int nslice = (steps + slices - 1) / slices * kAdStep;
-  return launch_chained(adapter_up_kernel<T, NR, MT>, dim3(tiles, (a.N + nslice - 1) / nslice), dim3(kAdThreads), 0,
-                        stream, (const T*)a.y.p, a.y.ld, a.T, a.N, a.r, a.n, (const T*)a.B, a.scale, a.perm, a.offsets,
-                        rest, p.parts, (const float*)a.part, nslice, (T*)a.out.p, a.out.ld);
+  const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM + (rest ? 1 : 0);  // at most this many
+  // as many blocks a tile as fill the machine twice and still have a step of k each
+  int cluster = 1;
+  while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * KG * 32) cluster *= 2;
+  const int kslice = ((a.K + cluster - 1) / cluster + 31) / 32 * 32;
+  const int nslice = ((a.N + cluster - 1) / cluster + 31) / 32 * 32;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_chained (moe_common.cuh)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)tiles * cluster);
+  cfg.blockDim = dim3(kAdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N, a.r, a.n,
+                            (const T*)a.A, (const T*)a.B, a.scale, a.perm, a.offsets, rest, cluster, kslice, nslice,
+                            (T*)a.out.p, a.out.ld);
 }
 
+// Tiles of 16 tokens for decode batches, where every row may be a request of its own; for
+// longer ones more tokens a tile the wider the rank, since a tile reads r (K + N) values of
+// its adapter beside its tokens' K + 2 N each.
 template <typename T>
-cudaError_t adapters_of(const AdapterPlan& p, const AdapterArgs& a, cudaStream_t s) {
-  switch (p.nr) {
-    case 2: return p.mt == 1 ? adapters_as<T, 2, 1>(p, a, s) : adapters_as<T, 2, 4>(p, a, s);
-    case 4: return p.mt == 1 ? adapters_as<T, 4, 1>(p, a, s) : adapters_as<T, 4, 4>(p, a, s);
-    case 8: return p.mt == 1 ? adapters_as<T, 8, 1>(p, a, s) : adapters_as<T, 8, 2>(p, a, s);
-    default: return adapters_as<T, 16, 1>(p, a, s);
-  }
+cudaError_t adapters_of(const AdapterArgs& a, cudaStream_t s) {
+  const bool few = a.T <= 128;
+  if (a.r <= 16) return few ? adapters_as<T, 2, 1>(a, s) : adapters_as<T, 2, 2>(a, s);
+  if (a.r <= 32) return few ? adapters_as<T, 4, 1>(a, s) : adapters_as<T, 4, 2>(a, s);
+  if (a.r <= 64) return few ? adapters_as<T, 8, 1>(a, s) : adapters_as<T, 8, 4>(a, s);
+  return few ? adapters_as<T, 16, 1>(a, s) : adapters_as<T, 16, 4>(a, s);
 }
 
 }  // namespace
 
-uint64_t adapters_ws_bytes(int T, int K, int r, int n) {
-  const AdapterPlan p = adapter_plan(T, K, r, n);
-  return up256((uint64_t)p.parts * T * r * 4 + 4);
-}
-
 cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t stream) {
-  const AdapterPlan p = adapter_plan(a.T, a.K, a.r, a.n);
-  return dtype == MOE_F16 ? adapters_of<__half>(p, a, stream) : adapters_of<__nv_bfloat16>(p, a, stream);
+  return dtype == MOE_F16 ? adapters_of<__half>(a, stream) : adapters_of<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace moe

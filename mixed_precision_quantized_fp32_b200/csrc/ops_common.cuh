@@ -124,9 +124,7 @@ struct AdapterArgs {
   const void *A, *B;
   const float* scale;
   const int32_t *perm, *offsets;
-  float* part;
 };
-uint64_t adapters_ws_bytes(int T, int K, int r, int n);
 cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t stream);
 
 }  // namespace moe

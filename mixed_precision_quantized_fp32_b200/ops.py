@@ -382,17 +382,8 @@ def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | N
 
 
 # ------------------------------------------------------------------ adapters
-@lru_cache(maxsize=4096)
-def adapters_workspace_bytes(T: int, K: int, N: int, r: int, n: int) -> int:
-    """Bytes of ws that moe_adapters needs."""
-    need = C.c_uint64(0)
-    check("moe_adapters(workspace query)", _lib.load().moe_adapters(
-        None, K, None, N, 0, T, K, N, r, n, None, None, None, None, None, None, N, None, 0, C.byref(need), None))
-    return need.value
-
-
 def moe_adapters(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
-                 routes: Routes, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                 routes: Routes, out: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """out = y + scale[a] * B[a] (A[a] x) for each token's adapter a (none: out = y).
 
@@ -417,11 +408,10 @@ def moe_adapters(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Ten
     if out is None:
         out = c.empty(y, (T, N), dt)
     op, ldo = c.rows(out, "out", T, N, dt)
-    ws, wp, wn = c.memory(ws, x, adapters_workspace_bytes(T, K, N, r, n))
-    c.run(_lib.load().moe_adapters, xp, ldx, yp, ldy, _DTYPE[dt], T, K, N, r, n, ap, bp, sp, pp, fp, op, ldo, wp, wn, None)
+    c.run(_lib.load().moe_adapters, xp, ldx, yp, ldy, _DTYPE[dt], T, K, N, r, n, ap, bp, sp, pp, fp, op, ldo)
     return out
 
 
-__all__ = ["ActCkpt", "Routes", "SwigluCkpt", "adapters_workspace_bytes", "alloc_ckpt", "alloc_routes", "moe_act_load",
+__all__ = ["ActCkpt", "Routes", "SwigluCkpt", "alloc_ckpt", "alloc_routes", "moe_act_load",
            "moe_act_save", "moe_adapters", "moe_collect", "moe_collect_backward", "moe_dispatch", "moe_dispatch_backward",
            "moe_sort", "moe_swiglu_backward", "moe_swiglu_save", "sort_workspace_bytes"]
