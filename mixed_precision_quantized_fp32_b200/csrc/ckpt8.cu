@@ -19,6 +19,8 @@
 // bf16 loads are 16 bytes and code stores 8 bytes a lane, consecutive over the warp, and
 // the group's maximum takes two shuffles.  Rows whose pitch or start does not allow that
 // run one lane per value.
+#include <initializer_list>
+
 #include "ops_common.cuh"
 
 namespace moe {
@@ -45,47 +47,90 @@ __device__ __forceinline__ float step_of(uint32_t eb) { return __uint_as_float(e
 
 // The code sits in the low byte of x * 2^-e + 1.5 * 2^23: that sum is rounded to a whole
 // number, to nearest even, by the addition itself.
-template <typename T>
-__device__ __forceinline__ uint32_t code_bits(float x, float inv, bool top) {
-  if (top) x = fminf(fmaxf(x * inv, -127.0f), 127.0f), inv = 1.0f;
+__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
   return __float_as_uint(fmaf(x, inv, 12582912.0f));
 }
+__device__ __forceinline__ float clamp127(float x) { return fminf(fmaxf(x, -127.0f), 127.0f); }
 
+// Codes of eight values.  Only the highest exponent can leave values beyond 127 steps, and
+// only 255 stands for values without codes: both take the branch.
 template <typename T>
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t eb) {
-  const float inv = inv_step(eb);
-  if (eb == 255u) return make_uint2(0u, 0u);
-  const bool top = eb == (uint32_t)(emax<T>() + 127);
   uint32_t c[8];
+  if (eb < (uint32_t)(emax<T>() + 127)) {
+    const float inv = inv_step(eb);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = code_bits<T>(v[i], inv, top);
+    for (int i = 0; i < 8; ++i) c[i] = code_bits(v[i], inv);
+  } else {
+    if (eb == 255u) return make_uint2(0u, 0u);
+    const float inv = inv_step(eb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = code_bits(clamp127(v[i] * inv), 1.0f);
+  }
   uint2 q;
   q.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   q.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
   return q;
 }
 
-__device__ __forceinline__ uint32_t abs_bits8(const float (&v)[8]) {
-  uint32_t m = 0;
+// Eight values as they lie in memory.
+template <typename T> struct Eight { uint4 a[sizeof(T) / 2]; };
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T* p) {
+  Eight<T> e;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.a[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return e;
 }
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+template <typename T>
+__device__ __forceinline__ void values8(const Eight<T>& e, float (&v)[8]) {
+  constexpr int N = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    float f[N];
+    decode_raw<T, N>(e.a[i], f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[N * i + j] = f[j];
+  }
 }
 
-// q * 2^e of four codes: byte + 2^23 as a float by one byte permute, then the offset off.
-__device__ __forceinline__ void decode4(uint32_t q, float step, float* v) {
-  q ^= 0x80808080u;  // q + 128
+// Largest |x| over the quad's 32 values as fp32 bits.  Magnitudes order as their bits do,
+// infinities and NaN on top, so the maximum is an integer one: of 16-bit halves two at once.
+template <typename T>
+__device__ __forceinline__ uint32_t quad_amax(const Eight<T>& e) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = (__uint_as_float(__byte_perm(q, 0x4B000000u, 0x7440 + i)) - 8388736.0f) * step;
+    for (int i = 0; i < 2; ++i)
+      m = max(m, max(max(e.a[i].x & 0x7FFFFFFFu, e.a[i].y & 0x7FFFFFFFu), max(e.a[i].z & 0x7FFFFFFFu, e.a[i].w & 0x7FFFFFFFu)));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  } else {
+    constexpr uint32_t A = 0x7FFF7FFFu;
+    uint32_t m = __vmaxu2(__vmaxu2(e.a[0].x & A, e.a[0].y & A), __vmaxu2(e.a[0].z & A, e.a[0].w & A));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(unpack2<T>(m).x);
+  }
 }
-__device__ __forceinline__ void decode8(uint2 q, float step, float (&v)[8]) {
-  decode4(q.x, step, v);
-  decode4(q.y, step, v + 4);
+
+// q * 2^e of eight codes.  One byte permute makes 2^23 + 128 + q as a float, one fused
+// multiply-add takes the offset off and scales; both are exact.  Steps of 2^103 and more,
+// where the offset times the step would overflow, and NaN groups multiply afterwards.
+__device__ __forceinline__ void decode8(uint2 q, uint32_t eb, float (&v)[8]) {
+  const float step = step_of(eb);
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  if (eb < 230u) {
+    const float off = -8388736.0f * step;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = fmaf(__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7440 + i % 4)), step, off);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = (__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7440 + i % 4)) - 8388736.0f) * step;
+  }
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
@@ -103,54 +148,93 @@ __device__ __forceinline__ Grads swiglu_grad(float g, float u, float dh) {
 
 // Where a lane works: group `at` of the rows in order, value `col` of row `row`.
 struct Place {
-  int64_t row;
-  int grp, col;
+  int64_t row, col;
+  int grp;
   bool in;  // the lane has values there
 };
 
 // ---------------------------------------------------------------- eight values a lane
-__device__ __forceinline__ Place place8(uint32_t at, int G, int rows, int F) {
-  Place p;
-  p.row = at / (uint32_t)G;
-  p.grp = (int)(at - (uint32_t)p.row * (uint32_t)G);
-  p.col = p.grp * kGroup + (threadIdx.x & 3) * 8;
-  p.in = p.row < rows && p.col < F;
-  return p;
-}
+// FLAT: F is a multiple of 32 and every matrix is without gaps, so the groups of all rows
+// follow one another and a lane's place needs no division by the groups a row.
+// A thread takes two places, 64 groups apart, with both places' loads in flight at once.
+constexpr int kPlaces = 2;
+constexpr int kGroupsPerBlock = 64 * kPlaces;
 
 __device__ __forceinline__ int row_count(int R, const int32_t* n_rows) {
   return n_rows ? min(R, max(0, __ldg(n_rows))) : R;
 }
 
-template <typename T>
+template <bool FLAT>
+__device__ __forceinline__ Place place8(int i, int G, int rows, int F) {
+  Place p;
+  const uint32_t at = blockIdx.x * (uint32_t)kGroupsPerBlock + i * 64u + (threadIdx.x >> 2);
+  if (FLAT) {
+    p.row = 0;
+    p.grp = (int)at;
+    p.col = (int64_t)at * kGroup + (threadIdx.x & 3) * 8;
+    p.in = at < (uint32_t)rows * (uint32_t)G;
+  } else {
+    const uint32_t row = at / (uint32_t)G;
+    p.row = row;
+    p.grp = (int)(at - row * (uint32_t)G);
+    p.col = p.grp * kGroup + (threadIdx.x & 3) * 8;
+    p.in = row < (uint32_t)rows && p.col < F;
+  }
+  return p;
+}
+
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) act_save_kernel(const T* __restrict__ x, int64_t ldx, int R, int F,
                                                        int8_t* __restrict__ q, uint8_t* __restrict__ ex,
                                                        const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place8(blockIdx.x * 64u + (threadIdx.x >> 2), G, rows, F);
-  float v[8] = {};
-  if (p.in) load_vec<T, 8>(x + p.row * ldx + p.col, v);
-  const uint32_t eb = group_exp<T>(quad_max(abs_bits8(v)));
-  if (!p.in) return;
-  *reinterpret_cast<uint2*>(q + p.row * F + p.col) = encode8<T>(v, eb);
-  if ((threadIdx.x & 3) == 0) ex[p.row * G + p.grp] = (uint8_t)eb;
+  Place p[kPlaces];
+  Eight<T> e[kPlaces];
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    p[i] = place8<FLAT>(i, G, rows, F);
+    e[i] = Eight<T>{};
+    if (p[i].in) e[i] = load8(x + p[i].row * ldx + p[i].col);
+  }
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    const uint32_t eb = group_exp<T>(quad_amax(e[i]));
+    if (!p[i].in) continue;
+    float v[8];
+    values8(e[i], v);
+    *reinterpret_cast<uint2*>(q + p[i].row * F + p[i].col) = encode8<T>(v, eb);
+    if ((threadIdx.x & 3) == 0) ex[p[i].row * G + p[i].grp] = (uint8_t)eb;
+  }
 }
 
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) act_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex,
                                                        int R, int F, T* __restrict__ x, int64_t ldx,
                                                        const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place8(blockIdx.x * 64u + (threadIdx.x >> 2), G, rows, F);
-  if (!p.in) return;
-  float v[8];
-  decode8(__ldg(reinterpret_cast<const uint2*>(q + p.row * F + p.col)), step_of(__ldg(ex + p.row * G + p.grp)), v);
-  store_vec<T, 8>(x + p.row * ldx + p.col, v);
+  Place p[kPlaces];
+  uint2 c[kPlaces];
+  uint32_t eb[kPlaces];
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    p[i] = place8<FLAT>(i, G, rows, F);
+    if (p[i].in) {
+      c[i] = __ldg(reinterpret_cast<const uint2*>(q + p[i].row * F + p[i].col));
+      eb[i] = __ldg(ex + p[i].row * G + p[i].grp);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    if (!p[i].in) continue;
+    float v[8];
+    decode8(c[i], eb[i], v);
+    store_vec<T, 8>(x + p[i].row * ldx + p[i].col, v);
+  }
 }
 
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) swiglu_save_kernel(const T* __restrict__ g, int64_t ldg, const T* __restrict__ u,
                                                           int64_t ldu, int R, int F, T* __restrict__ h, int64_t ldh,
                                                           int8_t* __restrict__ gq, uint8_t* __restrict__ ge,
@@ -158,48 +242,75 @@ __global__ void __launch_bounds__(256) swiglu_save_kernel(const T* __restrict__ 
                                                           const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place8(blockIdx.x * 64u + (threadIdx.x >> 2), G, rows, F);
-  float a[8] = {}, b[8] = {};
-  if (p.in) {
-    load_vec<T, 8>(g + p.row * ldg + p.col, a);
-    load_vec<T, 8>(u + p.row * ldu + p.col, b);
-  }
-  const uint32_t ea = group_exp<T>(quad_max(abs_bits8(a))), eb = group_exp<T>(quad_max(abs_bits8(b)));
-  if (!p.in) return;
-  const int64_t at = p.row * F + p.col;
-  *reinterpret_cast<uint2*>(gq + at) = encode8<T>(a, ea);
-  *reinterpret_cast<uint2*>(uq + at) = encode8<T>(b, eb);
-  if ((threadIdx.x & 3) == 0) {
-    ge[p.row * G + p.grp] = (uint8_t)ea;
-    ue[p.row * G + p.grp] = (uint8_t)eb;
+  Place p[kPlaces];
+  Eight<T> e[kPlaces], f[kPlaces];
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    p[i] = place8<FLAT>(i, G, rows, F);
+    e[i] = f[i] = Eight<T>{};
+    if (p[i].in) {
+      e[i] = load8(g + p[i].row * ldg + p[i].col);
+      f[i] = load8(u + p[i].row * ldu + p[i].col);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = swiglu(a[i], b[i]);
-  store_vec<T, 8>(h + p.row * ldh + p.col, a);
+  for (int i = 0; i < kPlaces; ++i) {
+    const uint32_t ea = group_exp<T>(quad_amax(e[i])), eb = group_exp<T>(quad_amax(f[i]));
+    if (!p[i].in) continue;
+    const int64_t at = p[i].row * F + p[i].col, ge_at = p[i].row * G + p[i].grp;
+    float a[8], b[8];
+    values8(e[i], a);
+    values8(f[i], b);
+    *reinterpret_cast<uint2*>(gq + at) = encode8<T>(a, ea);
+    *reinterpret_cast<uint2*>(uq + at) = encode8<T>(b, eb);
+    if ((threadIdx.x & 3) == 0) {
+      ge[ge_at] = (uint8_t)ea;
+      ue[ge_at] = (uint8_t)eb;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = swiglu(a[j], b[j]);
+    store_vec<T, 8>(h + p[i].row * ldh + p[i].col, a);
+  }
 }
 
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(256) swiglu_backward_kernel(
     const T* __restrict__ dh, int64_t lddh, const int8_t* __restrict__ gq, const uint8_t* __restrict__ ge,
     const int8_t* __restrict__ uq, const uint8_t* __restrict__ ue, int R, int F, T* __restrict__ dg, int64_t lddg,
     T* __restrict__ du, int64_t lddu, T* __restrict__ h, int64_t ldh, const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place8(blockIdx.x * 64u + (threadIdx.x >> 2), G, rows, F);
-  if (!p.in) return;
-  float d[8], a[8], b[8];
-  const int64_t at = p.row * F + p.col;
-  load_vec<T, 8>(dh + p.row * lddh + p.col, d);
-  decode8(__ldg(reinterpret_cast<const uint2*>(gq + at)), step_of(__ldg(ge + p.row * G + p.grp)), a);
-  decode8(__ldg(reinterpret_cast<const uint2*>(uq + at)), step_of(__ldg(ue + p.row * G + p.grp)), b);
+  Place p[kPlaces];
+  Eight<T> e[kPlaces];
+  uint2 cg[kPlaces], cu[kPlaces];
+  uint32_t eg[kPlaces], eu[kPlaces];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const Grads r = swiglu_grad(a[i], b[i], d[i]);
-    d[i] = r.dg, a[i] = r.du, b[i] = r.h;
+  for (int i = 0; i < kPlaces; ++i) {
+    p[i] = place8<FLAT>(i, G, rows, F);
+    if (!p[i].in) continue;
+    const int64_t at = p[i].row * F + p[i].col, ge_at = p[i].row * G + p[i].grp;
+    e[i] = load8(dh + p[i].row * lddh + p[i].col);
+    cg[i] = __ldg(reinterpret_cast<const uint2*>(gq + at));
+    cu[i] = __ldg(reinterpret_cast<const uint2*>(uq + at));
+    eg[i] = __ldg(ge + ge_at);
+    eu[i] = __ldg(ue + ge_at);
   }
-  store_vec<T, 8>(dg + p.row * lddg + p.col, d);
-  store_vec<T, 8>(du + p.row * lddu + p.col, a);
-  if (h) store_vec<T, 8>(h + p.row * ldh + p.col, b);
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    if (!p[i].in) continue;
+    float d[8], a[8], b[8];
+    values8(e[i], d);
+    decode8(cg[i], eg[i], a);
+    decode8(cu[i], eu[i], b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Grads r = swiglu_grad(a[j], b[j], d[j]);
+      d[j] = r.dg, a[j] = r.du, b[j] = r.h;
+    }
+    store_vec<T, 8>(dg + p[i].row * lddg + p[i].col, d);
+    store_vec<T, 8>(du + p[i].row * lddu + p[i].col, a);
+    if (h) store_vec<T, 8>(h + p[i].row * ldh + p[i].col, b);
+  }
 }
 
 // ---------------------------------------------------------------- one value a lane
@@ -219,7 +330,7 @@ __device__ __forceinline__ uint32_t warp_exp(float v) {
 template <typename T>
 __device__ __forceinline__ int8_t encode1(float v, uint32_t eb) {
   if (eb == 255u) return 0;
-  return (int8_t)(code_bits<T>(v, inv_step(eb), eb == (uint32_t)(emax<T>() + 127)) & 0xFFu);
+  return (int8_t)(code_bits(clamp127(v * inv_step(eb)), 1.0f) & 0xFFu);
 }
 
 template <typename T>
@@ -290,46 +401,61 @@ __global__ void __launch_bounds__(256) swiglu_backward1_kernel(
 // ---------------------------------------------------------------- host
 namespace {
 
-// Eight values a lane need 16-byte rows and codes on 8-byte boundaries.
-bool vec_rows(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 16 == 0; }
-bool vec_ckpt(const Ckpt& c, int F) { return F % 8 == 0 && ((uintptr_t)c.q & 7) == 0; }
+// How a call runs: one value a lane, eight, or eight with all rows in one.
+enum class Way { kOne, kEight, kFlat };
 
-unsigned blocks(int R, int F, int per) {
-  return (unsigned)(((uint64_t)R * ((F + kGroup - 1) / kGroup) + per - 1) / per);
+struct Matrix {
+  const void* p;
+  int64_t ld;
+};
+// Eight values a lane need 16-byte rows and codes on 8-byte boundaries.
+Way way_of(int es, int F, std::initializer_list<Matrix> rows, std::initializer_list<const void*> codes) {
+  bool eight = F % 8 == 0, flat = F % kGroup == 0;
+  for (const Matrix& m : rows) {
+    if (!m.p) continue;
+    eight = eight && on16(m.p) && (m.ld * es) % 16 == 0;
+    flat = flat && m.ld == F;
+  }
+  for (const void* c : codes) eight = eight && ((uintptr_t)c & 7) == 0;
+  return !eight ? Way::kOne : flat ? Way::kFlat : Way::kEight;
 }
+
+dim3 grid_of(Way w, int R, int F) {
+  const uint64_t groups = (uint64_t)R * ((F + kGroup - 1) / kGroup), per = w == Way::kOne ? 8 : kGroupsPerBlock;
+  return dim3((unsigned)((groups + per - 1) / per));
+}
+
+#define MOE_PICK(w, name, T) \
+  ((w) == Way::kOne ? name##1_kernel<T> : (w) == Way::kFlat ? name##_kernel<T, true> : name##_kernel<T, false>)
 
 template <typename T>
 cudaError_t save_as(ConstRows x, int R, int F, Ckpt c, const int32_t* n_rows, cudaStream_t s) {
-  const bool v = vec_rows(x.p, x.ld, sizeof(T)) && vec_ckpt(c, F);
-  return launch_chained(v ? act_save_kernel<T> : act_save1_kernel<T>, dim3(blocks(R, F, v ? 64 : 8)), dim3(256), 0, s,
-                        (const T*)x.p, x.ld, R, F, c.q, c.e, n_rows);
+  const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
+  return launch_chained(MOE_PICK(w, act_save, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)x.p, x.ld, R, F, c.q, c.e,
+                        n_rows);
 }
 template <typename T>
 cudaError_t load_as(Ckpt c, int R, int F, Rows x, const int32_t* n_rows, cudaStream_t s) {
-  const bool v = vec_rows(x.p, x.ld, sizeof(T)) && vec_ckpt(c, F);
-  return launch_chained(v ? act_load_kernel<T> : act_load1_kernel<T>, dim3(blocks(R, F, v ? 64 : 8)), dim3(256), 0, s,
-                        (const int8_t*)c.q, (const uint8_t*)c.e, R, F, (T*)x.p, x.ld, n_rows);
+  const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
+  return launch_chained(MOE_PICK(w, act_load, T), grid_of(w, R, F), dim3(256), 0, s, (const int8_t*)c.q,
+                        (const uint8_t*)c.e, R, F, (T*)x.p, x.ld, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_save_as(ConstRows g, ConstRows u, int R, int F, Rows h, Ckpt cg, Ckpt cu, const int32_t* n_rows,
                            cudaStream_t s) {
-  const bool v = vec_rows(g.p, g.ld, sizeof(T)) && vec_rows(u.p, u.ld, sizeof(T)) && vec_rows(h.p, h.ld, sizeof(T)) &&
-                 vec_ckpt(cg, F) && vec_ckpt(cu, F);
-  return launch_chained(v ? swiglu_save_kernel<T> : swiglu_save1_kernel<T>, dim3(blocks(R, F, v ? 64 : 8)), dim3(256),
-                        0, s, (const T*)g.p, g.ld, (const T*)u.p, u.ld, R, F, (T*)h.p, h.ld, cg.q, cg.e, cu.q, cu.e,
-                        n_rows);
+  const Way w = way_of(sizeof(T), F, {{g.p, g.ld}, {u.p, u.ld}, {h.p, h.ld}}, {cg.q, cu.q});
+  return launch_chained(MOE_PICK(w, swiglu_save, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)g.p, g.ld,
+                        (const T*)u.p, u.ld, R, F, (T*)h.p, h.ld, cg.q, cg.e, cu.q, cu.e, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_backward_as(ConstRows dh, Ckpt cg, Ckpt cu, int R, int F, Rows dg, Rows du, Rows h,
                                const int32_t* n_rows, cudaStream_t s) {
-  const bool v = vec_rows(dh.p, dh.ld, sizeof(T)) && vec_rows(dg.p, dg.ld, sizeof(T)) &&
-                 vec_rows(du.p, du.ld, sizeof(T)) && (!h.p || vec_rows(h.p, h.ld, sizeof(T))) && vec_ckpt(cg, F) &&
-                 vec_ckpt(cu, F);
-  return launch_chained(v ? swiglu_backward_kernel<T> : swiglu_backward1_kernel<T>, dim3(blocks(R, F, v ? 64 : 8)),
-                        dim3(256), 0, s, (const T*)dh.p, dh.ld, (const int8_t*)cg.q, (const uint8_t*)cg.e,
-                        (const int8_t*)cu.q, (const uint8_t*)cu.e, R, F, (T*)dg.p, dg.ld, (T*)du.p, du.ld, (T*)h.p,
-                        h.ld, n_rows);
+  const Way w = way_of(sizeof(T), F, {{dh.p, dh.ld}, {dg.p, dg.ld}, {du.p, du.ld}, {h.p, h.ld}}, {cg.q, cu.q});
+  return launch_chained(MOE_PICK(w, swiglu_backward, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)dh.p, dh.ld,
+                        (const int8_t*)cg.q, (const uint8_t*)cg.e, (const int8_t*)cu.q, (const uint8_t*)cu.e, R, F,
+                        (T*)dg.p, dg.ld, (T*)du.p, du.ld, (T*)h.p, h.ld, n_rows);
 }
+#undef MOE_PICK
 
 }  // namespace
 

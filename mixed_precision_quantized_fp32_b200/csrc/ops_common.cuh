@@ -77,6 +77,33 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
   }
 }
 
+// N consecutive values as they lie in memory, to have many loads on their way before the
+// first is used: 16 bytes (N = 8 of a 16-bit type, 4 of fp32), or one value (N = 1).
+template <typename T, int N> struct Raw { using type = uint4; };
+template <typename T> struct Raw<T, 1> { using type = T; };
+
+template <typename T, int N>
+__device__ __forceinline__ void decode_raw(const typename Raw<T, N>::type& q, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = to_f32<T>(q);
+  } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        v[j] = __uint_as_float(w[j]);
+      } else {
+        const float2 f = unpack2<T>(w[j]);
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+      }
+    }
+  }
+}
+template <typename R> __device__ __forceinline__ R zero_raw() {
+  if constexpr (sizeof(R) == 16) return make_uint4(0, 0, 0, 0);
+  else return R(0.0f);
+}
+
 inline int dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 

@@ -170,106 +170,166 @@ __global__ void __launch_bounds__(kSortBlock) sort_rank_kernel(const int32_t* __
   }
 }
 
-// One block per token: its row goes to each of its experts' rows.
-template <typename U>
+// Where a thread of the row kernels works.  A token's row is walked by P consecutive
+// threads (a power of two up to the block), so short rows share a block.
+struct Walk {
+  int64_t t;
+  int lane, P;
+};
+__device__ __forceinline__ Walk walk(int shift) {
+  return {(int64_t)blockIdx.x * (blockDim.x >> shift) + (threadIdx.x >> shift), (int)(threadIdx.x & ((1u << shift) - 1)),
+          1 << shift};
+}
+
+// A token's row goes to each of its experts' rows.  K: entries a token has at most, so
+// that the rows stay in registers.
+template <typename U, int K>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(const U* __restrict__ x, int64_t ldx,
-                                                            const int32_t* __restrict__ inv, int k, U* __restrict__ xs,
-                                                            int64_t ldxs, int n) {
+                                                            const int32_t* __restrict__ inv, int T, int k,
+                                                            U* __restrict__ xs, int64_t ldxs, int n, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int t = blockIdx.x;
-  int rows[kMaxK];
-  for (int j = 0; j < k; ++j) rows[j] = inv[(int64_t)t * k + j];
-  const U* src = x + (int64_t)t * ldx;
-  for (int c = threadIdx.x; c < n; c += blockDim.x) {
-    const U v = __ldg(src + c);
-    for (int j = 0; j < k; ++j)
-      if (rows[j] >= 0) xs[(int64_t)rows[j] * ldxs + c] = v;
+  const Walk w = walk(shift);
+  if (w.t >= T) return;
+  const U* src = x + w.t * ldx;
+  U* dst[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int row = j < k ? __ldg(inv + w.t * k + j) : -1;
+    dst[j] = row >= 0 ? xs + (int64_t)row * ldxs : nullptr;
+  }
+  for (int c = w.lane; c < n; c += 2 * w.P) {
+    const bool two = c + w.P < n;
+    const U a = __ldg(src + c), b = two ? __ldg(src + c + w.P) : a;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (dst[j]) {
+        dst[j][c] = a;
+        if (two) dst[j][c + w.P] = b;
+      }
   }
 }
 
-// Sum of a token's expert rows, weighted or not.
-template <typename T, int N>
+// Rows and weights of a token's entries; an entry without a row gets weight 0 and is not read.
+template <int K>
+__device__ __forceinline__ void entries_of(int64_t t, const int32_t* inv, const float* w, int R, int k, int (&rows)[K],
+                                           float (&wt)[K]) {
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    rows[j] = j < k ? __ldg(inv + t * k + j) : -1;
+    if ((unsigned)rows[j] >= (unsigned)R) rows[j] = -1;
+    wt[j] = rows[j] < 0 ? 0.0f : w ? __ldg(w + t * k + j) : 1.0f;
+  }
+}
+
+// Sum of a token's expert rows, weighted or not.  All K rows' loads (U pieces of each) are
+// on their way before the first sum.
+template <typename T, int N, int K, int U>
 __global__ void __launch_bounds__(256) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
                                                            const float* __restrict__ w,
-                                                           const int32_t* __restrict__ inv, int R, int k, int H,
-                                                           T* __restrict__ y, int64_t ldy) {
+                                                           const int32_t* __restrict__ inv, int T_, int k, int cols,
+                                                           T* __restrict__ y, int64_t ldy, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int64_t t = blockIdx.x;
-  int rows[kMaxK];
-  float wt[kMaxK];
+  using R = typename Raw<T, N>::type;
+  const Walk at = walk(shift);
+  if (at.t >= T_) return;
+  int rows[K];
+  float wt[K];
+  entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
+  for (int c = blockIdx.y * U * at.P + at.lane; c < cols; c += gridDim.y * U * at.P) {
+    R v[U][K];
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    rows[j] = j < k ? inv[t * k + j] : -1;
-    if ((unsigned)rows[j] >= (unsigned)R) rows[j] = -1;
-    wt[j] = (w && rows[j] >= 0) ? w[t * k + j] : 1.0f;
-  }
-  for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * N; c < H; c += gridDim.y * blockDim.x * N) {
-    float acc[N];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+      for (int j = 0; j < K; ++j)
+        v[u][j] = rows[j] >= 0 && c + u * at.P < cols
+                      ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j] * ldo) + c + u * at.P)
+                      : zero_raw<R>();
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j) {
-      if (rows[j] < 0) continue;
-      float v[N];
-      load_vec<T, N>(o + (int64_t)rows[j] * ldo + c, v);
+    for (int u = 0; u < U; ++u) {
+      if (c + u * at.P >= cols) break;
+      float acc[N] = {};
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[j], v[i], acc[i]);
+      for (int j = 0; j < K; ++j) {
+        float f[N];
+        decode_raw<T, N>(v[u][j], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[j], f[i], acc[i]);
+      }
+      store_vec<T, N>(y + at.t * ldy + (int64_t)(c + u * at.P) * N, acc);
     }
-    store_vec<T, N>(y + t * ldy + c, acc);
   }
 }
 
 // Gradient of collect: dy's row is read once, scaled into each expert row, and its dot
-// product with each expert's output summed over the block in a fixed order.
-template <typename T, int N>
+// product with each expert's output summed over the token's threads in a fixed order.
+template <typename T, int N, int K, int U>
 __global__ void __launch_bounds__(512) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
                                                                const T* __restrict__ o, int64_t ldo,
                                                                const float* __restrict__ w,
-                                                               const int32_t* __restrict__ inv, int R, int k, int H,
+                                                               const int32_t* __restrict__ inv, int T_, int k, int cols,
                                                                T* __restrict__ d_o, int64_t lddo,
-                                                               float* __restrict__ dw) {
+                                                               float* __restrict__ dw, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  __shared__ float part[16][kMaxK];
-  const int64_t t = blockIdx.x;
-  int rows[kMaxK];
-  float wt[kMaxK], dot[kMaxK];
+  using R = typename Raw<T, N>::type;
+  __shared__ float part[16][K];
+  const Walk at = walk(shift);
+  const bool real = at.t < T_;
+  int rows[K];
+  float wt[K], dot[K] = {};
+  if (real) {
+    entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
+    for (int c = at.lane; c < cols; c += U * at.P) {
+      R g[U], v[U][K];
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    rows[j] = j < k ? inv[t * k + j] : -1;
-    if ((unsigned)rows[j] >= (unsigned)R) rows[j] = -1;
-    wt[j] = rows[j] >= 0 ? w[t * k + j] : 0.0f;
-    dot[j] = 0.0f;
-  }
-  for (int c = threadIdx.x * N; c < H; c += blockDim.x * N) {
-    float g[N];
-    load_vec<T, N>(dy + t * lddy + c, g);
+      for (int u = 0; u < U; ++u) {
+        const bool in = c + u * at.P < cols;
+        g[u] = in ? __ldg(reinterpret_cast<const R*>(dy + at.t * lddy) + c + u * at.P) : zero_raw<R>();
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j) {
-      if (rows[j] < 0) continue;
-      float v[N], d[N];
-      load_vec<T, N>(o + (int64_t)rows[j] * ldo + c, v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        dot[j] = fmaf(g[i], v[i], dot[j]);
-        d[i] = wt[j] * g[i];
+        for (int j = 0; j < K; ++j)
+          v[u][j] = in && rows[j] >= 0 ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j] * ldo) + c + u * at.P)
+                                       : zero_raw<R>();
       }
-      store_vec<T, N>(d_o + (int64_t)rows[j] * lddo + c, d);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c + u * at.P >= cols) break;
+        float a[N];
+        decode_raw<T, N>(g[u], a);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          if (rows[j] < 0) continue;
+          float f[N], d[N];
+          decode_raw<T, N>(v[u][j], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[j] = fmaf(a[i], f[i], dot[j]);
+            d[i] = wt[j] * a[i];
+          }
+          store_vec<T, N>(d_o + (int64_t)rows[j] * lddo + (int64_t)(c + u * at.P) * N, d);
+        }
+      }
     }
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int within = at.P < 32 ? at.P : 32;  // threads of the token in this warp
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    if (j >= k) break;
+  for (int j = 0; j < K; ++j)
+    for (int s = within / 2; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+  if (at.P > 32) {  // the token's warps: their sums in order
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
-    if (lane == 0) part[warp][j] = dot[j];
+    for (int j = 0; j < K; ++j)
+      if (lane == 0) part[warp][j] = dot[j];
+    __syncthreads();
+    if (at.lane == 0)
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        dot[j] = 0.0f;
+        for (int q = 0; q < at.P / 32; ++q) dot[j] += part[warp + q][j];
+      }
   }
-  __syncthreads();
-  if (threadIdx.x < k) {
-    float s = 0.0f;
-    for (int q = 0; q < (int)(blockDim.x >> 5); ++q) s += part[q][threadIdx.x];
-    dw[t * k + threadIdx.x] = s;
-  }
+  if (real && at.lane == 0)
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (j < k) dw[at.t * k + j] = dot[j];
 }
 
 // ---------------------------------------------------------------- host
@@ -279,6 +339,14 @@ int sort_per_block(int R) {  // entries per block: a multiple of 1024, at most 1
   const int per = (R + kSortMaxBlocks - 1) / kSortMaxBlocks;
   return (per + kSortBlock - 1) / kSortBlock * kSortBlock;
 }
+
+// Threads that walk a row of n pieces, U at a time: a power of two from 8 to `most`, as its shift.
+int walk_shift(int n, int U, int most) {
+  int s = 3;
+  while ((1 << s) < most && (int64_t)(1 << s) * U < n) ++s;
+  return s;
+}
+unsigned walk_blocks(int T, int threads, int shift) { return (unsigned)((T + (threads >> shift) - 1) / (threads >> shift)); }
 
 template <typename U>
 cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, int32_t* inv, int32_t* offsets,
@@ -299,30 +367,50 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
   e = launch_chained(sort_rank_kernel, dim3(nblk), dim3(kSortBlock), (size_t)32 * (E + 1), stream, idx, R, per, E,
                      (const int32_t*)hist, perm, inv, offsets);
   if (e != cudaSuccess || !xp) return e;
-  const int threads = n >= 256 ? 256 : (n + 31) / 32 * 32;
-  return launch_chained(dispatch_rows_kernel<U>, dim3(T), dim3(threads), 0, stream, xp, ldx, (const int32_t*)inv, k,
-                        xsp, ldxs, n);
+  const int shift = walk_shift(n, 2, 256);
+  auto kern = k <= 2 ? dispatch_rows_kernel<U, 2> : k <= 4 ? dispatch_rows_kernel<U, 4> : dispatch_rows_kernel<U, 8>;
+  return launch_chained(kern, dim3(walk_blocks(T, 256, shift)), dim3(256), 0, stream, xp, ldx, (const int32_t*)inv, T,
+                        k, xsp, ldxs, n, shift);
 }
 
-template <typename T, int N>
+// U: pieces of each row in flight, so that K * U loads of 16 bytes (single values: four
+// times as many) are, within 128 registers.
+template <typename T, int N, int K>
 cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y,
                        cudaStream_t stream) {
-  const int cols = (H + N - 1) / N;
-  const int threads = cols >= 256 ? 256 : (cols + 31) / 32 * 32;
-  int ny = 1;  // column blocks: more parallelism for few tokens
-  while (T_ * ny < 592 && ny * threads < cols) ny *= 2;
-  return launch_chained(collect_rows_kernel<T, N>, dim3(T_, ny), dim3(threads), 0, stream, (const T*)o.p, o.ld, w, inv,
-                        T_ * k, k, H, (T*)y.p, y.ld);
+  constexpr int U = N == 1 ? 4 : K <= 4 ? 2 : 1;
+  const int cols = H / N, shift = walk_shift(cols, U, 256);
+  const unsigned blocks = walk_blocks(T_, 256, shift);
+  unsigned ny = 1;  // column blocks: more parallelism for few tokens
+  while (blocks * ny < 2 * 148 && (int64_t)ny * U * 256 < cols) ny *= 2;
+  return launch_chained(collect_rows_kernel<T, N, K, U>, dim3(blocks, ny), dim3(256), 0, stream, (const T*)o.p, o.ld, w,
+                        inv, T_, k, cols, (T*)y.p, y.ld, shift);
+}
+
+template <typename T, int N, int K>
+cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
+                                Rows d_o, float* dw, cudaStream_t stream) {
+  constexpr int U = N == 1 ? 4 : K <= 2 ? 2 : 1;
+  const int cols = H / N;
+  const int threads = T_ < 2 * 148 ? 512 : 256;  // few tokens: more threads a row
+  const int shift = walk_shift(cols, U, threads);
+  return launch_chained(collect_backward_kernel<T, N, K, U>, dim3(walk_blocks(T_, threads, shift)), dim3(threads), 0,
+                        stream, (const T*)dy.p, dy.ld, (const T*)o.p, o.ld, w, inv, T_, k, cols, (T*)d_o.p, d_o.ld, dw,
+                        shift);
 }
 
 template <typename T, int N>
-cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
-                                Rows d_o, float* dw, cudaStream_t stream) {
-  const int cols = (H + N - 1) / N;
-  const int most = T_ >= 592 ? 256 : 512;
-  const int threads = cols >= most ? most : (cols + 31) / 32 * 32;
-  return launch_chained(collect_backward_kernel<T, N>, dim3(T_), dim3(threads), 0, stream, (const T*)dy.p, dy.ld,
-                        (const T*)o.p, o.ld, w, inv, T_ * k, k, H, (T*)d_o.p, d_o.ld, dw);
+cudaError_t collect_k(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y, cudaStream_t s) {
+  return k <= 2   ? collect_as<T, N, 2>(o, w, inv, T_, k, H, y, s)
+         : k <= 4 ? collect_as<T, N, 4>(o, w, inv, T_, k, H, y, s)
+                  : collect_as<T, N, 8>(o, w, inv, T_, k, H, y, s);
+}
+template <typename T, int N>
+cudaError_t collect_backward_k(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
+                               Rows d_o, float* dw, cudaStream_t s) {
+  return k <= 2   ? collect_backward_as<T, N, 2>(dy, o, w, inv, T_, k, H, d_o, dw, s)
+         : k <= 4 ? collect_backward_as<T, N, 4>(dy, o, w, inv, T_, k, H, d_o, dw, s)
+                  : collect_backward_as<T, N, 8>(dy, o, w, inv, T_, k, H, d_o, dw, s);
 }
 
 bool rows16(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 16 == 0; }
@@ -350,12 +438,12 @@ cudaError_t launch_collect(ConstRows o, const float* w, const int32_t* inv, int 
   const int es = dtype_size(dtype);
   const bool vec = rows16(o.p, o.ld, es) && rows16(y.p, y.ld, es) && ((int64_t)H * es) % 16 == 0;
   if (dtype == MOE_F32)
-    return vec ? collect_as<float, 4>(o, w, inv, T, k, H, y, stream) : collect_as<float, 1>(o, w, inv, T, k, H, y, stream);
+    return vec ? collect_k<float, 4>(o, w, inv, T, k, H, y, stream) : collect_k<float, 1>(o, w, inv, T, k, H, y, stream);
   if (dtype == MOE_F16)
-    return vec ? collect_as<__half, 8>(o, w, inv, T, k, H, y, stream)
-               : collect_as<__half, 1>(o, w, inv, T, k, H, y, stream);
-  return vec ? collect_as<__nv_bfloat16, 8>(o, w, inv, T, k, H, y, stream)
-             : collect_as<__nv_bfloat16, 1>(o, w, inv, T, k, H, y, stream);
+    return vec ? collect_k<__half, 8>(o, w, inv, T, k, H, y, stream)
+               : collect_k<__half, 1>(o, w, inv, T, k, H, y, stream);
+  return vec ? collect_k<__nv_bfloat16, 8>(o, w, inv, T, k, H, y, stream)
+             : collect_k<__nv_bfloat16, 1>(o, w, inv, T, k, H, y, stream);
 }
 
 cudaError_t launch_collect_backward(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T, int k, int H,
@@ -364,13 +452,13 @@ cudaError_t launch_collect_backward(ConstRows dy, ConstRows o, const float* w, c
   const bool vec = rows16(dy.p, dy.ld, es) && rows16(o.p, o.ld, es) && rows16(d_o.p, d_o.ld, es) &&
                    ((int64_t)H * es) % 16 == 0;
   if (dtype == MOE_F32)
-    return vec ? collect_backward_as<float, 4>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-               : collect_backward_as<float, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+    return vec ? collect_backward_k<float, 4>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+               : collect_backward_k<float, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
   if (dtype == MOE_F16)
-    return vec ? collect_backward_as<__half, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-               : collect_backward_as<__half, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
-  return vec ? collect_backward_as<__nv_bfloat16, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-             : collect_backward_as<__nv_bfloat16, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+    return vec ? collect_backward_k<__half, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+               : collect_backward_k<__half, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+  return vec ? collect_backward_k<__nv_bfloat16, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
+             : collect_backward_k<__nv_bfloat16, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
 }
 
 }  // namespace moe
