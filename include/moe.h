@@ -376,7 +376,7 @@ enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
  * offsets: DEVICE i32 [E+1]; group e has rows [offsets[e], offsets[e+1]);
  *   offsets[E] = rows that have a group.
  * ws: DEVICE, 256-byte aligned; ws == NULL with ws_bytes_out -> *ws_bytes_out = the
- *   size needed for (T, k, E) and nothing runs.  T*k <= 1024 needs none (size 0):
+ *   size needed for (T, k, E) and nothing runs.  T*k <= 16384 needs none (size 0):
  *   ws and ws_bytes_out may both be NULL then.
  * Limits: 1 <= k <= 8, T*k <= 2^20, 1 <= E <= MOE_MAX_GROUPS.
  * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_SHAPE, MOE_ERR_WORKSPACE,

@@ -104,22 +104,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
-// A float of block `rank`'s shared memory at the place that p has in this block's.
-__device__ __forceinline__ float load_remote(const float* p, uint32_t rank) {
-  uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
-
 // NR: n8 tiles of the rank (r <= 8*NR).  MT: m16 tiles of tokens; the 8 warps are MT token
 // tiles times 8/MT shares of k, then of the outputs.
 template <typename T, int NR, int MT>
@@ -212,7 +196,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
       if (i < r && row < tile.rows) {
         const float* p = mine + row * NR * 8 + i;
         if (cluster > 1)
-          for (int b = 0; b < cluster; ++b) s += load_remote(p, b);
+          for (int b = 0; b < cluster; ++b) s += __uint_as_float(load_remote(p, b));
         else
           s = *p;
         s *= sc;
@@ -321,21 +305,10 @@ cudaError_t adapters_as(const AdapterArgs& a, cudaStream_t stream) {
   while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * KG * 32) cluster *= 2;
   const int kslice = ((a.K + cluster - 1) / cluster + 31) / 32 * 32;
   const int nslice = ((a.N + cluster - 1) / cluster + 31) / 32 * 32;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_chained (moe_common.cuh)
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)tiles * cluster);
-  cfg.blockDim = dim3(kAdThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N, a.r, a.n,
-                            (const T*)a.A, (const T*)a.B, a.scale, a.perm, a.offsets, rest, cluster, kslice, nslice,
-                            (T*)a.out.p, a.out.ld);
+  return launch_cluster(kern, dim3((unsigned)tiles * cluster), dim3(kAdThreads), cluster, smem, stream,
+                        (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N, a.r, a.n, (const T*)a.A,
+                        (const T*)a.B, a.scale, a.perm, a.offsets, rest, cluster, kslice, nslice, (T*)a.out.p,
+                        a.out.ld);
 }
 
 // Tiles of 16 tokens for decode batches, where every row may be a request of its own; for

@@ -21,6 +21,10 @@ namespace moe {
 constexpr int kSortSmall = 1024;   // entries that one launch sorts by counting
 constexpr int kSortBlock = 1024;
 constexpr int kSortMaxBlocks = 128;
+constexpr int kSortCluster = 8;    // blocks of the cluster that sorts more
+constexpr int kSortRounds = 2;     // keys a lane of it holds
+constexpr int kSortMedium = kSortCluster * kSortBlock * kSortRounds;
+static_assert(kMaxGroups <= kSortBlock, "the cluster's scan takes the keys in at most two steps");
 
 __device__ __forceinline__ int sort_key(int32_t e, int E) { return (unsigned)e < (unsigned)E ? e : E; }
 
@@ -89,7 +93,114 @@ __global__ void __launch_bounds__(256) dispatch_small_kernel(const int32_t* __re
   if (x && key < E) copy_row(x + (int64_t)(i / k) * ldx, xs + (int64_t)row * ldxs, n);
 }
 
-// Pass 1 over `per` entries a block: histogram of the keys.
+// Inclusive scan over a block of 1024 threads.  wsum: 32 words of shared memory.
+__device__ __forceinline__ int block_scan(int v, int32_t* wsum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto warp_scan = [&](int s) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    return s;
+  };
+  const int s = warp_scan(v);
+  if (lane == 31) wsum[warp] = s;
+  __syncthreads();
+  if (warp == 0) {  // the warps' sums become what lies before each warp
+    const int w = wsum[lane];
+    wsum[lane] = warp_scan(w) - w;
+  }
+  __syncthreads();
+  return wsum[warp] + s;
+}
+
+// Up to 16384 entries in one launch of one cluster, without a workspace.  Each of its 256
+// warps owns consecutive entries and keeps its lanes' keys (at most two) in registers:
+//   - a warp ranks its entries among its own, 32 at a time, with a count per key;
+//   - per key, the warps' counts become offsets within the block, the blocks' totals are
+//     read over distributed shared memory, and the totals are scanned over the keys;
+//   - row = start of the key + earlier blocks + earlier warps + rank.
+// The scattered stores of perm bound it to what 8 SMs can do: at 16384 entries of 256 groups
+// it takes as long as the two launches below, at 49152 4 us more.
+__global__ void __launch_bounds__(kSortBlock) sort_cluster_kernel(const int32_t* __restrict__ idx, int R, int per,
+                                                                  int E, int32_t* __restrict__ perm,
+                                                                  int32_t* __restrict__ inv,
+                                                                  int32_t* __restrict__ offsets) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  extern __shared__ uint16_t wcount[];  // [32][E+1]: entries of each key in each warp, then the earlier warps'
+  __shared__ int32_t total[kMaxGroups + 1], base[kMaxGroups + 1];
+  __shared__ int32_t wsum[kSortBlock / 32], carry;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int lo = (int)(rank * (kSortBlock / 32) + warp) * per, hi = min(R, lo + per);
+  int key[kSortRounds], below[kSortRounds];
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const int at = lo + 32 * i + lane;
+    key[i] = 32 * i < per && at < hi ? sort_key(__ldg(idx + at), E) : -1;
+  }
+  for (int c = tid; c < 16 * (E + 1); c += kSortBlock) reinterpret_cast<uint32_t*>(wcount)[c] = 0;
+  __syncthreads();
+  uint16_t* mine = wcount + warp * (E + 1);
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    if (32 * i >= per) break;
+    const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+    const int lower = __popc(same & ((1u << lane) - 1u));
+    const int before = key[i] >= 0 ? mine[key[i]] : 0;
+    below[i] = before + lower;
+    __syncwarp();
+    if (key[i] >= 0 && lower == 0) mine[key[i]] = (uint16_t)(before + __popc(same));
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = tid; e <= E; e += kSortBlock) {
+    int run = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortBlock / 32; ++w) {
+      const int c = wcount[w * (E + 1) + e];
+      wcount[w * (E + 1) + e] = (uint16_t)run;
+      run += c;
+    }
+    total[e] = run;
+  }
+  cluster_arrive();
+  cluster_wait();
+  int run = 0;
+  for (int e0 = 0; e0 <= E; e0 += kSortBlock) {
+    const int e = e0 + tid;
+    int all = 0, earlier = 0;
+    if (e <= E) {
+#pragma unroll
+      for (int b = 0; b < kSortCluster; ++b) {
+        const int v = (int)load_remote(&total[e], b);
+        all += v;
+        earlier += b < (int)rank ? v : 0;
+      }
+    }
+    const int off = run + block_scan(all, wsum) - all;
+    if (e <= E) {
+      base[e] = off + earlier;
+      if (rank == 0) offsets[e] = off;
+    }
+    if (tid == kSortBlock - 1) carry = off + all;  // read again only where E = 1024: one more key follows
+    __syncthreads();
+    run = carry;
+  }
+  cluster_arrive();  // totals have been read; a block may not leave before the others have
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    if (key[i] < 0) continue;
+    const int at = lo + 32 * i + lane;
+    const int row = base[key[i]] + mine[key[i]] + below[i];
+    perm[row] = at;
+    inv[at] = key[i] < E ? row : -1;
+  }
+  cluster_wait();
+}
+
+// More entries: pass 1 over `per` entries a block, histogram of the keys.
 __global__ void __launch_bounds__(kSortBlock) sort_hist_kernel(const int32_t* __restrict__ idx, int R, int per, int E,
                                                                int32_t* __restrict__ blk_hist) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
@@ -102,67 +213,74 @@ __global__ void __launch_bounds__(kSortBlock) sort_hist_kernel(const int32_t* __
   for (int e = threadIdx.x; e <= E; e += kSortBlock) blk_hist[(size_t)blockIdx.x * (E + 1) + e] = hist[e];
 }
 
-// Pass 2: every block sums the histograms before its own (and all of them, for the
-// offsets), then ranks its entries 1024 at a time: rank = entries of the key in earlier
-// warps + lower lanes with the key.
+// Pass 2: every block sums the histograms of all blocks, and of those before its own, with
+// its threads in groups of blocks; then it ranks its entries 1024 at a time as the cluster does.
 __global__ void __launch_bounds__(kSortBlock) sort_rank_kernel(const int32_t* __restrict__ idx, int R, int per, int E,
                                                                const int32_t* __restrict__ blk_hist,
                                                                int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                                                                int32_t* __restrict__ offsets) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   extern __shared__ uint8_t wcnt[];  // [32][E+1]: entries of each key in each warp
-  __shared__ int32_t base[kMaxGroups + 1];
-  __shared__ int32_t wsum[kSortBlock / 32];
+  __shared__ int32_t total[kMaxGroups + 1], base[kMaxGroups + 1];
+  __shared__ int32_t wsum[kSortBlock / 32], carry;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lo = blockIdx.x * per, hi = min(R, lo + per);
+  int next = lo + tid < hi ? __ldg(idx + lo + tid) : 0;  // the first entries, on their way meanwhile
+  for (int e = tid; e <= E; e += kSortBlock) total[e] = base[e] = 0;
+  __syncthreads();
+  // warps w, w + 32/groups, ... of one part of the keys each sum a share of the blocks
+  const int parts = (E + 32) / 32;                   // 32 keys a warp at once
+  const int shares = max(1, (kSortBlock / 32) / parts);
+  for (int job = warp; job < parts * shares; job += kSortBlock / 32) {
+    const int e = (job % parts) * 32 + lane, share = job / parts;
+    int all = 0, before = 0;
+    if (e <= E) {
+#pragma unroll 8
+      for (int b = share; b < (int)gridDim.x; b += shares) {
+        const int v = __ldg(blk_hist + (size_t)b * (E + 1) + e);
+        all += v;
+        before += b < (int)blockIdx.x ? v : 0;
+      }
+      atomicAdd(&total[e], all);  // integer sums: any order
+      atomicAdd(&base[e], before);
+    }
+  }
+  __syncthreads();
   int run = 0;
   for (int e0 = 0; e0 <= E; e0 += kSortBlock) {
     const int e = e0 + tid;
-    int total = 0, mine = 0;
+    const int all = e <= E ? total[e] : 0;
+    const int off = run + block_scan(all, wsum) - all;
     if (e <= E) {
-#pragma unroll 8
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int v = __ldg(blk_hist + (size_t)b * (E + 1) + e);
-        total += v;
-        mine += b < (int)blockIdx.x ? v : 0;
-      }
-    }
-    int s = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane == 31) wsum[warp] = s;
-    __syncthreads();
-    int before = run;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (e <= E) {
-      const int off = before + s - total;
-      base[e] = off + mine;
+      base[e] += off;
       if (blockIdx.x == 0) offsets[e] = off;
     }
-    for (int w = 0; w < kSortBlock / 32; ++w) run += wsum[w];
+    if (tid == kSortBlock - 1) carry = off + all;  // read again only where E = 1024: one more key follows
     __syncthreads();
+    run = carry;
   }
-  const int lo = blockIdx.x * per, hi = min(R, lo + per);
   for (int i0 = lo; i0 < hi; i0 += kSortBlock) {
     for (int c = tid; c < 8 * (E + 1); c += kSortBlock) reinterpret_cast<uint32_t*>(wcnt)[c] = 0;  // 32 * (E+1) bytes
-    __syncthreads();
     const int i = i0 + tid;
-    const int key = i < hi ? sort_key(idx[i], E) : -1;
+    const int key = i < hi ? sort_key(next, E) : -1;
+    next = i + kSortBlock < hi ? __ldg(idx + i + kSortBlock) : 0;
+    __syncthreads();
     const unsigned same = __match_any_sync(0xffffffffu, key);
     const int below = __popc(same & ((1u << lane) - 1u));
     if (key >= 0 && below == 0) wcnt[warp * (E + 1) + key] = (uint8_t)__popc(same);
     __syncthreads();
     if (key >= 0) {
       int row = base[key] + below;
+#pragma unroll 4
       for (int w = 0; w < warp; ++w) row += wcnt[w * (E + 1) + key];
       perm[row] = i;
       inv[i] = key < E ? row : -1;
     }
+    if (i0 + kSortBlock >= hi) break;
     __syncthreads();
     for (int e = tid; e <= E; e += kSortBlock) {
       int s = 0;
+#pragma unroll 8
       for (int w = 0; w < kSortBlock / 32; ++w) s += wcnt[w * (E + 1) + e];
       base[e] += s;
     }
@@ -221,49 +339,53 @@ __device__ __forceinline__ void entries_of(int64_t t, const int32_t* inv, const 
   }
 }
 
-// Sum of a token's expert rows, weighted or not.  All K rows' loads (U pieces of each) are
-// on their way before the first sum.
+// Sum of a token's expert rows, weighted or not.  U pieces of J rows are on their way
+// before the first sum.
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
+__global__ void __launch_bounds__(256, K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
                                                            const float* __restrict__ w,
                                                            const int32_t* __restrict__ inv, int T_, int k, int cols,
                                                            T* __restrict__ y, int64_t ldy, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   using R = typename Raw<T, N>::type;
+  constexpr int J = K < 4 ? K : 4;
   const Walk at = walk(shift);
   if (at.t >= T_) return;
   int rows[K];
   float wt[K];
   entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
   for (int c = blockIdx.y * U * at.P + at.lane; c < cols; c += gridDim.y * U * at.P) {
-    R v[U][K];
+    float acc[U][N] = {};
+#pragma unroll
+    for (int j0 = 0; j0 < K; j0 += J) {
+      R v[U][J];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          v[u][j] = rows[j0 + j] >= 0 && c + u * at.P < cols
+                        ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j0 + j] * ldo) + c + u * at.P)
+                        : zero_raw<R>();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          float f[N];
+          decode_raw<T, N>(v[u][j], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[u][i] = fmaf(wt[j0 + j], f[i], acc[u][i]);
+        }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        v[u][j] = rows[j] >= 0 && c + u * at.P < cols
-                      ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j] * ldo) + c + u * at.P)
-                      : zero_raw<R>();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u * at.P >= cols) break;
-      float acc[N] = {};
-#pragma unroll
-      for (int j = 0; j < K; ++j) {
-        float f[N];
-        decode_raw<T, N>(v[u][j], f);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[j], f[i], acc[i]);
-      }
-      store_vec<T, N>(y + at.t * ldy + (int64_t)(c + u * at.P) * N, acc);
-    }
+      if (c + u * at.P < cols) store_vec<T, N>(y + at.t * ldy + (int64_t)(c + u * at.P) * N, acc[u]);
   }
 }
 
 // Gradient of collect: dy's row is read once, scaled into each expert row, and its dot
 // product with each expert's output summed over the token's threads in a fixed order.
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(512) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
+__global__ void __launch_bounds__(256, K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
                                                                const T* __restrict__ o, int64_t ldo,
                                                                const float* __restrict__ w,
                                                                const int32_t* __restrict__ inv, int T_, int k, int cols,
@@ -271,7 +393,8 @@ __global__ void __launch_bounds__(512) collect_backward_kernel(const T* __restri
                                                                float* __restrict__ dw, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   using R = typename Raw<T, N>::type;
-  __shared__ float part[16][K];
+  constexpr int J = K < 8 ? 2 : 4;
+  __shared__ float part[8][K];
   const Walk at = walk(shift);
   const bool real = at.t < T_;
   int rows[K];
@@ -279,32 +402,37 @@ __global__ void __launch_bounds__(512) collect_backward_kernel(const T* __restri
   if (real) {
     entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
     for (int c = at.lane; c < cols; c += U * at.P) {
-      R g[U], v[U][K];
+      R g[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = c + u * at.P < cols;
-        g[u] = in ? __ldg(reinterpret_cast<const R*>(dy + at.t * lddy) + c + u * at.P) : zero_raw<R>();
+      for (int u = 0; u < U; ++u)
+        g[u] = c + u * at.P < cols ? __ldg(reinterpret_cast<const R*>(dy + at.t * lddy) + c + u * at.P) : zero_raw<R>();
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-          v[u][j] = in && rows[j] >= 0 ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j] * ldo) + c + u * at.P)
-                                       : zero_raw<R>();
-      }
+      for (int j0 = 0; j0 < K; j0 += J) {
+        R v[U][J];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (c + u * at.P >= cols) break;
-        float a[N];
-        decode_raw<T, N>(g[u], a);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-          if (rows[j] < 0) continue;
-          float f[N], d[N];
-          decode_raw<T, N>(v[u][j], f);
+          for (int j = 0; j < J; ++j)
+            v[u][j] = rows[j0 + j] >= 0 && c + u * at.P < cols
+                          ? __ldg(reinterpret_cast<const R*>(o + (int64_t)rows[j0 + j] * ldo) + c + u * at.P)
+                          : zero_raw<R>();
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[j] = fmaf(a[i], f[i], dot[j]);
-            d[i] = wt[j] * a[i];
+        for (int u = 0; u < U; ++u) {
+          if (c + u * at.P >= cols) break;
+          float a[N];
+          decode_raw<T, N>(g[u], a);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            if (rows[j0 + j] < 0) continue;
+            float f[N], d[N];
+            decode_raw<T, N>(v[u][j], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot[j0 + j] = fmaf(a[i], f[i], dot[j0 + j]);
+              d[i] = wt[j0 + j] * a[i];
+            }
+            store_vec<T, N>(d_o + (int64_t)rows[j0 + j] * lddo + (int64_t)(c + u * at.P) * N, d);
           }
-          store_vec<T, N>(d_o + (int64_t)rows[j] * lddo + (int64_t)(c + u * at.P) * N, d);
         }
       }
     }
@@ -340,6 +468,26 @@ int sort_per_block(int R) {  // entries per block: a multiple of 1024, at most 1
   return (per + kSortBlock - 1) / kSortBlock * kSortBlock;
 }
 
+cudaError_t sort_medium(const int32_t* idx, int R, int E, int32_t* perm, int32_t* inv, int32_t* offsets,
+                        cudaStream_t stream) {
+  const int warps = kSortCluster * kSortBlock / 32, per = ((R + warps - 1) / warps + 31) / 32 * 32;
+  const size_t smem = (size_t)64 * (E + 1);
+  const cudaError_t e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             64 * (kMaxGroups + 1));
+  if (e != cudaSuccess) return e;
+  return launch_cluster(sort_cluster_kernel, dim3(kSortCluster), dim3(kSortBlock), kSortCluster, smem, stream, idx, R,
+                        per, E, perm, inv, offsets);
+}
+
+cudaError_t sort_large(const int32_t* idx, int R, int E, int32_t* perm, int32_t* inv, int32_t* offsets, int32_t* hist,
+                       cudaStream_t stream) {
+  const int per = sort_per_block(R), nblk = (R + per - 1) / per;
+  const cudaError_t e = launch_chained(sort_hist_kernel, dim3(nblk), dim3(kSortBlock), 0, stream, idx, R, per, E, hist);
+  if (e != cudaSuccess) return e;
+  return launch_chained(sort_rank_kernel, dim3(nblk), dim3(kSortBlock), (size_t)32 * (E + 1), stream, idx, R, per, E,
+                        (const int32_t*)hist, perm, inv, offsets);
+}
+
 // Threads that walk a row of n pieces, U at a time: a power of two from 8 to `most`, as its shift.
 int walk_shift(int n, int U, int most) {
   int s = 3;
@@ -360,12 +508,8 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
   if (R <= kSortSmall)
     return launch_chained(dispatch_small_kernel<U>, dim3(R + 1), dim3(256), 0, stream, idx, R, k, E, perm, inv, offsets,
                           xp, ldx, xsp, ldxs, n);
-  int32_t* hist = (int32_t*)ws;
-  const int per = sort_per_block(R), nblk = (R + per - 1) / per;
-  cudaError_t e = launch_chained(sort_hist_kernel, dim3(nblk), dim3(kSortBlock), 0, stream, idx, R, per, E, hist);
-  if (e != cudaSuccess) return e;
-  e = launch_chained(sort_rank_kernel, dim3(nblk), dim3(kSortBlock), (size_t)32 * (E + 1), stream, idx, R, per, E,
-                     (const int32_t*)hist, perm, inv, offsets);
+  cudaError_t e = R <= kSortMedium ? sort_medium(idx, R, E, perm, inv, offsets, stream)
+                                   : sort_large(idx, R, E, perm, inv, offsets, (int32_t*)ws, stream);
   if (e != cudaSuccess || !xp) return e;
   const int shift = walk_shift(n, 2, 256);
   auto kern = k <= 2 ? dispatch_rows_kernel<U, 2> : k <= 4 ? dispatch_rows_kernel<U, 4> : dispatch_rows_kernel<U, 8>;
@@ -378,7 +522,7 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
 template <typename T, int N, int K>
 cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y,
                        cudaStream_t stream) {
-  constexpr int U = N == 1 ? 4 : K <= 4 ? 2 : 1;
+  constexpr int U = N == 1 ? 4 : 2;
   const int cols = H / N, shift = walk_shift(cols, U, 256);
   const unsigned blocks = walk_blocks(T_, 256, shift);
   unsigned ny = 1;  // column blocks: more parallelism for few tokens
@@ -390,12 +534,11 @@ cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, 
 template <typename T, int N, int K>
 cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
                                 Rows d_o, float* dw, cudaStream_t stream) {
-  constexpr int U = N == 1 ? 4 : K <= 2 ? 2 : 1;
+  constexpr int U = N == 1 ? 4 : 2;
   const int cols = H / N;
-  const int threads = T_ < 2 * 148 ? 512 : 256;  // few tokens: more threads a row
-  const int shift = walk_shift(cols, U, threads);
-  return launch_chained(collect_backward_kernel<T, N, K, U>, dim3(walk_blocks(T_, threads, shift)), dim3(threads), 0,
-                        stream, (const T*)dy.p, dy.ld, (const T*)o.p, o.ld, w, inv, T_, k, cols, (T*)d_o.p, d_o.ld, dw,
+  const int shift = walk_shift(cols, U, 256);
+  return launch_chained(collect_backward_kernel<T, N, K, U>, dim3(walk_blocks(T_, 256, shift)), dim3(256), 0, stream,
+                        (const T*)dy.p, dy.ld, (const T*)o.p, o.ld, w, inv, T_, k, cols, (T*)d_o.p, d_o.ld, dw,
                         shift);
 }
 
@@ -418,7 +561,7 @@ bool rows16(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 1
 }  // namespace
 
 uint64_t sort_ws_bytes(int R, int E) {
-  if (R <= kSortSmall) return 0;
+  if (R <= kSortMedium) return 0;
   const int per = sort_per_block(R);
   return up256((uint64_t)((R + per - 1) / per) * (E + 1) * 4);
 }

@@ -82,7 +82,8 @@ def check_routes(r, idx, E):
 @pytest.mark.parametrize("T,k,E,kind", [
     (0, 2, 8, "all"), (1, 1, 1, "all"), (1, 8, 8, "all"), (16, 6, 256, "all"), (33, 3, 5, "holes"),
     (128, 8, 256, "padded"), (1024, 1, 1024, "outside"), (205, 5, 7, "holes"), (1025, 1, 1, "all"),
-    (513, 2, 256, "none"), (700, 2, 64, "one"), (4097, 8, 256, "outside"), (20000, 7, 1000, "padded"),
+    (513, 2, 256, "none"), (700, 2, 64, "one"), (4097, 8, 256, "outside"), (8193, 1, 1023, "holes"),
+    (3000, 3, 1024, "outside"), (16384, 1, 1024, "holes"), (16385, 1, 1024, "holes"), (16384, 3, 33, "holes"), (20000, 7, 1000, "padded"),
     (131072, 8, 128, "holes")])
 def test_sort(T, k, E, kind):
     idx = index(T, k, E, kind)

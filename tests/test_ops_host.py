@@ -107,14 +107,14 @@ def test_alignment(name):
             assert call(name, **{key: 68}) == "MOE_ERR_ALIGN", key
 
 
-@pytest.mark.parametrize("name,big", [("moe_sort", dict(T=3000)), ("moe_dispatch", dict(T=3000))])
+@pytest.mark.parametrize("name,big", [("moe_sort", dict(T=40000)), ("moe_dispatch", dict(T=40000))])
 def test_workspaces(name, big):
     n = need(name, **big)
     assert n >= 256 and n % 256 == 0
     assert call(name, ws_bytes=n - 1, **big) == "MOE_ERR_WORKSPACE"
     assert need(name) <= n
-    assert need(name, T=512) == 0 and need(name, T=513) > 0   # few entries: no workspace
-    assert torch.cuda.is_available() or call(name, T=512, ws=None, ws_bytes=0) in OK
+    assert need(name, T=8192) == 0 and need(name, T=8193) > 0   # few entries: no workspace
+    assert torch.cuda.is_available() or call(name, T=8192, ws=None, ws_bytes=0) in OK
     assert call(name, ws=None, need=None, **big) == "MOE_ERR_ARG"
 
 
