@@ -25,6 +25,10 @@ namespace moe {
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = 32 * kAdWarps;
 constexpr int kAdMaxCluster = 8;
+#ifndef XSHORT
+#define XSHORT 128
+#define XPER 16
+#endif
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -104,6 +108,50 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
+// The eight values at p, a lane's share of 32 of the rank, as the MMA's first operand (h: row
+// g or g + 8): pairs 0, 1 to the first MMA, 2, 3 to the second, as B's.
+template <typename T>
+__device__ __forceinline__ void split8(const float* p, int h, uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
+  const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+  split2<T>(u.x, u.y, hi[0][h], lo[0][h]);
+  split2<T>(u.z, u.w, hi[0][2 + h], lo[0][2 + h]);
+  split2<T>(v.x, v.y, hi[1][h], lo[1][h]);
+  split2<T>(v.z, v.w, hi[1][2 + h], lo[1][2 + h]);
+}
+
+// fp16: rows of P brought to at most 2^14 by a power of two, which undo[row] takes back.
+template <typename T>
+__device__ __forceinline__ void scale_rows(float* P, int ld, int width, int rows, float* undo) {
+  if constexpr (is_f16<T>) {
+    const int lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < rows; row += kAdWarps) {
+      uint32_t big = 0;
+      for (int i = lane; i < width; i += 32) big = max(big, __float_as_uint(P[row * ld + i]) & 0x7FFFFFFFu);
+      big = __reduce_max_sync(0xffffffffu, big);
+      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
+      const bool scaled = big < 0x7F800000u && e > 0;
+      if (scaled)
+        for (int i = lane; i < width; i += 32) P[row * ld + i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+      if (lane == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+    }
+    __syncthreads();
+  }
+}
+
+// y + back * acc for a lane's eight outputs of row g (h = 0) or g + 8 (h = 1).
+template <typename T>
+__device__ __forceinline__ void store_sum(T* out, const uint4& y, const float (&acc)[4][4], int h, float back) {
+  const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<T>(w[i]);
+    v[i] = pack2<T>(fmaf(back, acc[i][2 * h], f.x), fmaf(back, acc[i][2 * h + 1], f.y));
+  }
+  *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ---------------------------------------------------------------- decode batches
 // NR: n8 tiles of the rank (r <= 8*NR).  MT: m16 tiles of tokens; the 8 warps are MT token
 // tiles times 8/MT shares of k, then of the outputs.
 template <typename T, int NR, int MT>
@@ -205,31 +253,11 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     }
     if (cluster > 1) cluster_arrive();  // this block has read; it may not leave before the others have
     __syncthreads();
-    if constexpr (is_f16<T>) {
-      for (int row = warp; row < TM; row += kAdWarps) {
-        uint32_t big = 0;
-        for (int i = lane; i < RP; i += 32) big = max(big, __float_as_uint(P[row * LD + i]) & 0x7FFFFFFFu);
-        big = __reduce_max_sync(0xffffffffu, big);
-        const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-        const bool scaled = big < 0x7F800000u && e > 0;
-        if (scaled)
-          for (int i = lane; i < RP; i += 32) P[row * LD + i] *= __uint_as_float((uint32_t)(127 - e) << 23);
-        if (lane == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
-      }
-      __syncthreads();
-    }
+    scale_rows<T>(P, LD, RP, TM, undo);
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float* p = P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q;
-        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-        // lane's eight values: pairs 0, 1 to the first MMA, 2, 3 to the second (as B's)
-        split2<T>(u.x, u.y, hi[b][0][h], lo[b][0][h]);
-        split2<T>(u.z, u.w, hi[b][0][2 + h], lo[b][0][2 + h]);
-        split2<T>(v.x, v.y, hi[b][1][h], lo[b][1][h]);
-        split2<T>(v.z, v.w, hi[b][1][2 + h], lo[b][1][2 + h]);
-      }
+      for (int h = 0; h < 2; ++h) split8<T>(P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q, h, hi[b], lo[b]);
   }
   float back[2] = {1.0f, 1.0f};
   if constexpr (is_f16<T>) {
@@ -273,27 +301,230 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (tok[h] < 0 || col >= n1) continue;
-      const uint32_t w[4] = {yv[h].x, yv[h].y, yv[h].z, yv[h].w};
-      uint32_t v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<T>(w[i]);
-        v[i] = has ? pack2<T>(fmaf(back[h], acc[i][2 * h], f.x), fmaf(back[h], acc[i][2 * h + 1], f.y)) : w[i];
-      }
-      *reinterpret_cast<uint4*>(out + (int64_t)tok[h] * ldo + col) = make_uint4(v[0], v[1], v[2], v[3]);
+      T* o = out + (int64_t)tok[h] * ldo + col;
+      if (has)
+        store_sum<T>(o, yv[h], acc, h, back[h]);
+      else
+        *reinterpret_cast<uint4*>(o) = yv[h];
     }
   }
   if (has && cluster > 1) cluster_wait();
 }
 
+// ---------------------------------------------------------------- long batches
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {  // zeros where `in` is false
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Tiles of 64 tokens of one adapter.  The same two products and the same split over a
+// cluster, but operands come through a ring of 64-wide stages in shared memory (x and A,
+// then y and B, one ring over both products), since a tile's loads no longer fit in
+// registers ahead of their use.  Warps: 4 token tiles times 2 halves of a stage.
+// Rows of a stage are 128 bytes (B's: the rank); a lane reads the 16 bytes at chunk q of
+// its half in row g, and odd rows have their halves swapped, so the eight lanes of a
+// phase hit eight different 16-byte columns.
+constexpr int kWideStages = 4;
+constexpr int kWideTokens = 64;
+
+template <int NR> constexpr int wide_stage_bytes() { return kWideTokens * 128 + NR * 8 * 128; }
+template <int NR> constexpr int wide_smem_bytes() {
+  return kWideStages * wide_stage_bytes<NR>() + kWideTokens * NR * 8 * 4 + kWideTokens * (NR * 8 + 4) * 4 + kWideTokens * 4;
+}
+
+template <typename T, int NR>
+__global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
+    adapter_wide_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r,
+                        int n, const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
+                        const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
+                        int kslice, int nslice, T* out, int64_t ldo) {
+  pdl_enter();  // before any global memory access (see moe_common.cuh)
+  constexpr int TM = kWideTokens, KB = NR / 4, RP = NR * 8, LD = RP + 4, BROW = RP * 2;  // B's row in bytes
+  constexpr int STAGE = wide_stage_bytes<NR>();
+  extern __shared__ __align__(128) uint8_t wide_sm[];
+  uint8_t* ring = wide_sm;
+  float* mine = reinterpret_cast<float*>(ring + kWideStages * STAGE);  // [TM][RP] this block's share of P
+  float* P = mine + TM * RP;                                          // [TM][LD]
+  float* undo = P + TM * LD;                                          // [TM] fp16: takes a row's power of two back
+  const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, rest);
+  if (tile.rows == 0) return;  // all blocks of the cluster alike
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int m = warp & 3, half = warp >> 2;
+  const int k0 = rank * kslice, k1 = min(K, k0 + kslice), n0 = rank * nslice, n1 = min(N, n0 + nslice);
+  auto token = [&](int row) {
+    const int t = row < tile.rows ? __ldg(perm + tile.row0 + row) : -1;
+    return (unsigned)t < (unsigned)T_ ? t : -1;
+  };
+  const int chunk = tid & 7, row8 = tid >> 3;  // what the thread copies: 16-byte chunk of rows row8, row8 + 32
+  const int src[2] = {token(row8), token(row8 + 32)};
+  if (tile.adapter >= n) {  // rows without an adapter
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (src[h] >= 0)
+        for (int c = n0 + chunk * 8; c < n1; c += 64)
+          *reinterpret_cast<uint4*>(out + (int64_t)src[h] * ldo + c) =
+              __ldg(reinterpret_cast<const uint4*>(y + (int64_t)src[h] * ldy + c));
+    return;
+  }
+  const int tok[2] = {token(16 * m + g), token(16 * m + 8 + g)};
+  const T* Aa = A + (int64_t)tile.adapter * r * K;
+  const T* Ba = B + (int64_t)tile.adapter * N * r;
+  const int down = k1 > k0 ? (k1 - k0 + 63) / 64 : 0, up = n1 > n0 ? (n1 - n0 + 63) / 64 : 0;
+  auto issue = [&](int st) {
+    uint8_t* base = ring + (st & (kWideStages - 1)) * STAGE;
+    if (st < down) {
+      const int k = k0 + st * 64 + chunk * 8;
+      const bool in = k < k1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row8 + 32 * h;
+        copy16(base + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), src[h] >= 0 ? x + (int64_t)src[h] * ldx + (in ? k : 0) : x,
+               in && src[h] >= 0);
+      }
+#pragma unroll
+      for (int j = 0; j < NR / 4; ++j) {
+        const int row = row8 + 32 * j;
+        const bool real = in && row < r;
+        copy16(base + TM * 128 + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), real ? Aa + (int64_t)row * K + k : Aa, real);
+      }
+    } else if (st < down + up) {
+      const int c0 = n0 + (st - down) * 64, c = c0 + chunk * 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row8 + 32 * h;
+        const bool in = c < n1 && src[h] >= 0;
+        copy16(base + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), in ? y + (int64_t)src[h] * ldy + c : y, in);
+      }
+      // NR chunks a row: NR/4 a thread
+#pragma unroll
+      for (int j = 0; j < NR / 4; ++j) {
+        const int i = tid + kAdThreads * j, row = i / NR, b = i % NR;
+        const bool in = c0 + row < n1 && b * 8 < r;
+        copy16(base + TM * 128 + row * BROW + ((NR >= 8 ? b ^ ((row & 1) * 4) : b) * 16),
+               in ? Ba + (int64_t)(c0 + row) * r + b * 8 : Ba, in);
+      }
+    }
+    copy_commit();
+  };
+  // 16 bytes at chunk c of row `row` of a tile with `pitch` bytes a row
+  auto piece = [](const uint8_t* base, int row, int c, int pitch) {
+    return *reinterpret_cast<const uint4*>(base + row * pitch + ((pitch >= 128 ? c ^ ((row & 1) * 4) : c) * 16));
+  };
+#pragma unroll
+  for (int st = 0; st < kWideStages - 1; ++st) issue(st);
+  uint32_t hi[KB][2][4], lo[KB][2][4];
+  {
+    float acc[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    for (int st = 0; st < down; ++st) {
+      copy_wait<kWideStages - 2>();
+      __syncthreads();
+      issue(st + kWideStages - 1);
+      const uint8_t* xs = ring + (st & (kWideStages - 1)) * STAGE;
+      const uint8_t* as = xs + TM * 128;
+      const uint4 a = piece(xs, 16 * m + g, 4 * half + q, 128), b = piece(xs, 16 * m + 8 + g, 4 * half + q, 128);
+      const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint4 w = piece(as, 8 * i + g, 4 * half + q, 128);
+        mma16816<T>(acc[i], a0, w.x, w.y);
+        mma16816<T>(acc[i], a1, w.z, w.w);
+      }
+    }
+    // the two halves, then the blocks, each added in order
+    auto share = [&](int h, int i) {
+      return reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * RP + 8 * i + 2 * q);
+    };
+    if (half == 1)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) *share(h, i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+    __syncthreads();
+    if (half == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float2 o = *share(h, i);
+          *share(h, i) = make_float2(acc[i][2 * h] + o.x, acc[i][2 * h + 1] + o.y);
+        }
+  }
+  if (cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  const float sc = __ldg(scale + tile.adapter);
+  for (int c = tid; c < TM * RP; c += kAdThreads) {
+    const int row = c / RP, i = c % RP;
+    float s = 0.0f;
+    if (i < r && row < tile.rows) {
+      const float* p = mine + row * RP + i;
+      if (cluster > 1)
+        for (int b = 0; b < cluster; ++b) s += __uint_as_float(load_remote(p, b));
+      else
+        s = *p;
+      s *= sc;
+    }
+    P[row * LD + i] = s;
+  }
+  if (cluster > 1) cluster_arrive();  // this block has read; it may not leave before the others have
+  __syncthreads();
+  scale_rows<T>(P, LD, RP, TM, undo);
+#pragma unroll
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) split8<T>(P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q, h, hi[b], lo[b]);
+  float back[2] = {1.0f, 1.0f};
+  if constexpr (is_f16<T>)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) back[h] = undo[16 * m + 8 * h + g];
+  for (int st = down; st < down + up; ++st) {
+    copy_wait<kWideStages - 2>();
+    __syncthreads();
+    issue(st + kWideStages - 1);
+    const uint8_t* ys = ring + (st & (kWideStages - 1)) * STAGE;
+    const uint8_t* bs = ys + TM * 128;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = piece(bs, 32 * half + 8 * (g >> 1) + 2 * i + (g & 1), 4 * b + q, BROW);
+        mma16816<T>(acc[i], lo[b][0], w.x, w.y);
+        mma16816<T>(acc[i], lo[b][1], w.z, w.w);
+        mma16816<T>(acc[i], hi[b][0], w.x, w.y);
+        mma16816<T>(acc[i], hi[b][1], w.z, w.w);
+      }
+    const int col = n0 + (st - down) * 64 + 32 * half + 8 * q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (tok[h] < 0 || col >= n1) continue;
+      store_sum<T>(out + (int64_t)tok[h] * ldo + col, piece(ys, 16 * m + 8 * h + g, 4 * half + q, 128), acc, h, back[h]);
+    }
+  }
+  copy_wait<0>();
+  if (cluster > 1) cluster_wait();
+}
+
 // ---------------------------------------------------------------- host
 namespace {
 
-template <typename T, int NR, int MT>
-cudaError_t adapters_as(const AdapterArgs& a, cudaStream_t stream) {
-  constexpr int TM = 16 * MT, KG = kAdWarps / MT, KB = (NR + 3) / 4;
-  constexpr int smem = ((KG + 1) * TM * NR * 8 + TM * (KB * 32 + 4) + TM) * (int)sizeof(float);
-  auto kern = adapter_kernel<T, NR, MT>;
+template <typename T, typename Kern>
+cudaError_t adapters_with(Kern kern, int TM, int kstep, int smem, const AdapterArgs& a, cudaStream_t stream) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -302,7 +533,7 @@ cudaError_t adapters_as(const AdapterArgs& a, cudaStream_t stream) {
   const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM + (rest ? 1 : 0);  // at most this many
   // as many blocks a tile as fill the machine twice and still have a step of k each
   int cluster = 1;
-  while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * KG * 32) cluster *= 2;
+  while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * kstep) cluster *= 2;
   const int kslice = ((a.K + cluster - 1) / cluster + 31) / 32 * 32;
   const int nslice = ((a.N + cluster - 1) / cluster + 31) / 32 * 32;
   return launch_cluster(kern, dim3((unsigned)tiles * cluster), dim3(kAdThreads), cluster, smem, stream,
@@ -311,16 +542,27 @@ cudaError_t adapters_as(const AdapterArgs& a, cudaStream_t stream) {
                         a.out.ld);
 }
 
-// Tiles of 16 tokens for decode batches, where every row may be a request of its own; for
-// longer ones more tokens a tile the wider the rank, since a tile reads r (K + N) values of
-// its adapter beside its tokens' K + 2 N each.
+template <typename T, int NR>
+cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
+  constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4) + 16) * (int)sizeof(float);
+  return adapters_with<T>(adapter_kernel<T, NR, 1>, 16, kAdWarps * 32, smem, a, s);
+}
+template <typename T, int NR>
+cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
+  return adapters_with<T>(adapter_wide_kernel<T, NR>, kWideTokens, 64, wide_smem_bytes<NR>(), a, s);
+}
+
+// Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of
+// many adapters); tiles of 64 where adapters have rows enough to fill them.
 template <typename T>
 cudaError_t adapters_of(const AdapterArgs& a, cudaStream_t s) {
-  const bool few = a.T <= 128;
-  if (a.r <= 16) return few ? adapters_as<T, 2, 1>(a, s) : adapters_as<T, 2, 2>(a, s);
-  if (a.r <= 32) return few ? adapters_as<T, 4, 1>(a, s) : adapters_as<T, 4, 2>(a, s);
-  if (a.r <= 64) return few ? adapters_as<T, 8, 1>(a, s) : adapters_as<T, 8, 4>(a, s);
-  return few ? adapters_as<T, 16, 1>(a, s) : adapters_as<T, 16, 4>(a, s);
+  if (a.T <= XSHORT || a.T < XPER * a.n) {
+    if (a.r <= 16) return adapters_short<T, 2>(a, s);
+    if (a.r <= 32) return adapters_short<T, 4>(a, s);
+    return a.r <= 64 ? adapters_short<T, 8>(a, s) : adapters_short<T, 16>(a, s);
+  }
+  if (a.r <= 32) return adapters_wide<T, 4>(a, s);
+  return a.r <= 64 ? adapters_wide<T, 8>(a, s) : adapters_wide<T, 16>(a, s);
 }
 
 }  // namespace

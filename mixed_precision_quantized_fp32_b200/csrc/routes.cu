@@ -316,13 +316,16 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const U* __restrict_
     dst[j] = row >= 0 ? xs + (int64_t)row * ldxs : nullptr;
   }
   for (int c = w.lane; c < n; c += 2 * w.P) {
-    const bool two = c + w.P < n;
-    const U a = __ldg(src + c), b = two ? __ldg(src + c + w.P) : a;
+    U v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (c + u * w.P < n) v[u] = __ldg(src + c + u * w.P);
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (dst[j]) {
-        dst[j][c] = a;
-        if (two) dst[j][c + w.P] = b;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (c + u * w.P < n) dst[j][c + u * w.P] = v[u];
       }
   }
 }
