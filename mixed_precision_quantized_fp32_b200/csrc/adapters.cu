@@ -35,15 +35,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -138,6 +136,20 @@ __device__ __forceinline__ void scale_rows(float* P, int ld, int width, int rows
   }
 }
 
+// 32 of the rank times 32 outputs, small terms first; the four sums are independent.
+template <typename T>
+__device__ __forceinline__ void mma_hi_lo(float (&acc)[4][4], const uint32_t (&hi)[2][4], const uint32_t (&lo)[2][4],
+                                          const uint4 (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma16816<T>(acc[i], lo[0], w[i].x, w[i].y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma16816<T>(acc[i], lo[1], w[i].z, w[i].w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma16816<T>(acc[i], hi[0], w[i].x, w[i].y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma16816<T>(acc[i], hi[1], w[i].z, w[i].w);
+}
+
 // y + back * acc for a lane's eight outputs of row g (h = 0) or g + 8 (h = 1).
 template <typename T>
 __device__ __forceinline__ void store_sum(T* out, const uint4& y, const float (&acc)[4][4], int h, float back) {
@@ -211,10 +223,9 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
         w[i] = in && 8 * i < r ? __ldg(reinterpret_cast<const uint4*>(Ar + (int64_t)8 * i * K + kk)) : zero;
       const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        mma16816<T>(acc[i], a0, w[i].x, w[i].y);
-        mma16816<T>(acc[i], a1, w[i].z, w[i].w);
-      }
+      for (int i = 0; i < NR; ++i) mma16816<T>(acc[i], a0, w[i].x, w[i].y);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) mma16816<T>(acc[i], a1, w[i].z, w[i].w);
     }
     // the warps' shares, then the blocks', each added in order
     float* mr = red + part * TM * NR * 8;
@@ -289,13 +300,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
           bv[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk))
                                    : make_uint4(0, 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma16816<T>(acc[i], lo[b][0], bv[i].x, bv[i].y);
-          mma16816<T>(acc[i], lo[b][1], bv[i].z, bv[i].w);
-          mma16816<T>(acc[i], hi[b][0], bv[i].x, bv[i].y);
-          mma16816<T>(acc[i], hi[b][1], bv[i].z, bv[i].w);
-        }
+        mma_hi_lo<T>(acc, hi[b], lo[b], bv);
       }
     }
 #pragma unroll
@@ -431,11 +436,16 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
       const uint8_t* as = xs + TM * 128;
       const uint4 a = piece(xs, 16 * m + g, 4 * half + q, 128), b = piece(xs, 16 * m + 8 + g, 4 * half + q, 128);
       const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
+      constexpr int PART = NR < 8 ? NR : 8;  // independent sums between two that depend on one another
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const uint4 w = piece(as, 8 * i + g, 4 * half + q, 128);
-        mma16816<T>(acc[i], a0, w.x, w.y);
-        mma16816<T>(acc[i], a1, w.z, w.w);
+      for (int i0 = 0; i0 < NR; i0 += PART) {
+        uint4 w[PART];
+#pragma unroll
+        for (int i = 0; i < PART; ++i) w[i] = piece(as, 8 * (i0 + i) + g, 4 * half + q, 128);
+#pragma unroll
+        for (int i = 0; i < PART; ++i) mma16816<T>(acc[i0 + i], a0, w[i].x, w[i].y);
+#pragma unroll
+        for (int i = 0; i < PART; ++i) mma16816<T>(acc[i0 + i], a1, w[i].z, w[i].w);
       }
     }
     // the two halves, then the blocks, each added in order
@@ -500,15 +510,12 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
+    for (int b = 0; b < KB; ++b) {
+      uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 w = piece(bs, 32 * half + 8 * (g >> 1) + 2 * i + (g & 1), 4 * b + q, BROW);
-        mma16816<T>(acc[i], lo[b][0], w.x, w.y);
-        mma16816<T>(acc[i], lo[b][1], w.z, w.w);
-        mma16816<T>(acc[i], hi[b][0], w.x, w.y);
-        mma16816<T>(acc[i], hi[b][1], w.z, w.w);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = piece(bs, 32 * half + 8 * (g >> 1) + 2 * i + (g & 1), 4 * b + q, BROW);
+      mma_hi_lo<T>(acc, hi[b], lo[b], w);
+    }
     const int col = n0 + (st - down) * 64 + 32 * half + 8 * q;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
