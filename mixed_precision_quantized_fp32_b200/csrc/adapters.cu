@@ -53,21 +53,20 @@ struct Tile {
   int adapter, row0, rows;  // rows 0: none
 };
 
-// Tile `want` of the sorted rows: each adapter's rows in tiles of TM, adapters in order;
-// with `rest`, the rows behind the last adapter's follow as adapter n.  Every thread
-// takes a run of adapters and the block scans their tile counts.
-__device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets, int n, int T, bool rest) {
+// Tile `want` of the sorted rows: each adapter's rows in tiles of TM, adapters in order.
+// Every thread takes a run of adapters and the block scans their tile counts.
+__device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets, int n, int T) {
   __shared__ int wsum[kAdWarps];
   __shared__ Tile found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int segs = n + (rest ? 1 : 0), per = (segs + kAdThreads - 1) / kAdThreads;
+  const int per = (n + kAdThreads - 1) / kAdThreads;
   if (tid == 0) found = {0, 0, 0};
   auto lo_of = [&](int a) { return min(max(__ldg(offsets + a), 0), T); };
-  auto hi_of = [&](int a, int lo) { return a < n ? min(max(__ldg(offsets + a + 1), lo), T) : T; };
+  auto hi_of = [&](int a, int lo) { return min(max(__ldg(offsets + a + 1), lo), T); };
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int a = tid * per + i;
-    if (a >= segs) break;
+    if (a >= n) break;
     const int lo = lo_of(a);
     mine += (hi_of(a, lo) - lo + TM - 1) / TM;
   }
@@ -84,7 +83,7 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
   if (want >= before && want < before + mine) {
     for (int i = 0; i < per; ++i) {
       const int a = tid * per + i;
-      if (a >= segs) break;
+      if (a >= n) break;
       const int lo = lo_of(a), hi = hi_of(a, lo), tiles = (hi - lo + TM - 1) / TM;
       if (want < before + tiles) {
         const int r0 = lo + (want - before) * TM;
@@ -98,6 +97,30 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
   return found;
 }
 
+// out = y for the rows without an adapter, those behind the last adapter's: a share of them
+// for every warp, whether its block has a tile or not, eight pieces of a row in flight.
+template <typename T>
+__device__ void copy_rest(const T* y, int64_t ldy, T* out, int64_t ldo, int N, int n, int T_,
+                          const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets) {
+  const int lane = threadIdx.x & 31, first = min(max(__ldg(offsets + n), 0), T_);
+  const int block = gridDim.x - 1 - blockIdx.x;  // the last blocks have no tile, if any
+  for (int row = first + block * kAdWarps + (threadIdx.x >> 5); row < T_; row += gridDim.x * kAdWarps) {
+    const int t = __ldg(perm + row);
+    if ((unsigned)t >= (unsigned)T_) continue;
+    const uint4* from = reinterpret_cast<const uint4*>(y + (int64_t)t * ldy);
+    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)t * ldo);
+    for (int c = lane; c < N / 8; c += 256) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + 32 * i < N / 8) v[i] = __ldg(from + c + 32 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + 32 * i < N / 8) to[c + 32 * i] = v[i];
+    }
+  }
+}
+
 // Two values as hi and lo terms of T; an infinity stays one (inf - inf would be NaN).
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -106,33 +129,79 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
-// The eight values at p, a lane's share of 32 of the rank, as the MMA's first operand (h: row
-// g or g + 8): pairs 0, 1 to the first MMA, 2, 3 to the second, as B's.
+// Eight values of a lane, its share of 32 of the rank, as the MMA's first operand (h: row g or
+// g + 8): pairs 0, 1 to the first MMA, 2, 3 to the second, as B's.
 template <typename T>
-__device__ __forceinline__ void split8(const float* p, int h, uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
-  const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-  split2<T>(u.x, u.y, hi[0][h], lo[0][h]);
-  split2<T>(u.z, u.w, hi[0][2 + h], lo[0][2 + h]);
-  split2<T>(v.x, v.y, hi[1][h], lo[1][h]);
-  split2<T>(v.z, v.w, hi[1][2 + h], lo[1][2 + h]);
+__device__ __forceinline__ void split8(const float (&p)[8], int h, uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
+  split2<T>(p[0], p[1], hi[0][h], lo[0][h]);
+  split2<T>(p[2], p[3], hi[0][2 + h], lo[0][2 + h]);
+  split2<T>(p[4], p[5], hi[1][h], lo[1][h]);
+  split2<T>(p[6], p[7], hi[1][2 + h], lo[1][2 + h]);
 }
 
-// fp16: rows of P brought to at most 2^14 by a power of two, which undo[row] takes back.
-template <typename T>
-__device__ __forceinline__ void scale_rows(float* P, int ld, int width, int rows, float* undo) {
-  if constexpr (is_f16<T>) {
-    const int lane = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < rows; row += kAdWarps) {
-      uint32_t big = 0;
-      for (int i = lane; i < width; i += 32) big = max(big, __float_as_uint(P[row * ld + i]) & 0x7FFFFFFFu);
-      big = __reduce_max_sync(0xffffffffu, big);
-      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-      const bool scaled = big < 0x7F800000u && e > 0;
-      if (scaled)
-        for (int i = lane; i < width; i += 32) P[row * ld + i] *= __uint_as_float((uint32_t)(127 - e) << 23);
-      if (lane == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+// Adds the blocks' shares of P in order: every thread takes 16-byte pieces, whose remote
+// loads are consecutive over the warp.  mine: [TM][RP] in every block; P: [TM][KB*32 + 4],
+// zeros beyond the rank and behind the tile's rows.
+template <int TM, int KB, int RP>
+__device__ __forceinline__ void gather_p(const float* mine, int cluster, float scale, int r, int rows, float* P) {
+  constexpr int LD = KB * 32 + 4, PIECES = KB * 8;
+#pragma unroll
+  for (int c0 = 0; c0 < TM * PIECES; c0 += kAdThreads) {
+    const int c = c0 + threadIdx.x, row = c / PIECES, i = (c % PIECES) * 4;
+    if (TM * PIECES % kAdThreads != 0 && c >= TM * PIECES) break;
+    float4 s = make_float4(0, 0, 0, 0);
+    if (i < r && row < rows) {  // the rank is a multiple of 8
+      float4 v[kAdMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kAdMaxCluster; ++k)
+        if (k < cluster) v[k] = load_remote4(mine + row * RP + i, k);
+#pragma unroll
+      for (int k = 0; k < kAdMaxCluster; ++k)
+        if (k < cluster) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+      s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
     }
-    __syncthreads();
+    *reinterpret_cast<float4*>(P + row * LD + i) = s;
+  }
+}
+
+// A lane's share of P as the up product's operand: rows g and g + 8 of the token tile at P.
+// back: what takes a row's power of two back (fp16; else 1).
+template <typename T, int KB>
+__device__ __forceinline__ void operand_p(const float* P, uint32_t (&hi)[KB][2][4], uint32_t (&lo)[KB][2][4],
+                                          float (&back)[2]) {
+  constexpr int LD = KB * 32 + 4;
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float p[KB][8];
+    uint32_t big = 0;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(P + (8 * h + g) * LD + 32 * b + 8 * q + i);
+        p[b][i] = v.x, p[b][i + 1] = v.y, p[b][i + 2] = v.z, p[b][i + 3] = v.w;
+      }
+    back[h] = 1.0f;
+    if constexpr (is_f16<T>) {  // the row's four lanes agree on its power of two
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(p[b][i]) & 0x7FFFFFFFu);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
+      if (big < 0x7F800000u && e > 0) {
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        back[h] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[b][i] *= down;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < KB; ++b) split8<T>(p[b], h, hi[b], lo[b]);
   }
 }
 
@@ -164,44 +233,43 @@ __device__ __forceinline__ void store_sum(T* out, const uint4& y, const float (&
 }
 
 // ---------------------------------------------------------------- decode batches
-// NR: n8 tiles of the rank (r <= 8*NR).  MT: m16 tiles of tokens; the 8 warps are MT token
-// tiles times 8/MT shares of k, then of the outputs.
-template <typename T, int NR, int MT>
+// Tiles of 16 tokens; NR: n8 tiles of the rank (r <= 8*NR).  The 8 warps share the block's k
+// values, 32 at a time, then its outputs.
+template <typename T, int NR>
 __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     adapter_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r, int n,
                    const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
                    const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
                    int kslice, int nslice, T* out, int64_t ldo) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  constexpr int TM = 16 * MT, KG = kAdWarps / MT, KB = (NR + 3) / 4, RP = KB * 32, LD = RP + 4;
-  extern __shared__ float sm[];
-  float* red = sm;                            // [KG][TM][NR*8] shares of the warps
-  float* mine = red + KG * TM * NR * 8;       // [TM][NR*8] this block's share of P
-  float* P = mine + TM * NR * 8;              // [TM][LD]
-  float* undo = P + TM * LD;                  // [TM] fp16: what takes a row's power of two back
-  const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
-  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, rest);
-  if (tile.rows == 0) return;  // all blocks of the cluster alike
+  constexpr int TM = 16, KG = kAdWarps, KB = (NR + 3) / 4, RP = NR * 8;
+  extern __shared__ __align__(16) float sm[];
+  float* red = sm;                  // [KG][TM][RP] shares of the warps
+  float* mine = red + KG * TM * RP;  // [TM][RP] this block's share of P
+  float* P = mine + TM * RP;         // [TM][KB*32 + 4]
+  const uint32_t rank = cluster_rank();
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_);
+  if (tile.rows == 0) {  // all blocks of the cluster alike
+    if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int m = warp % MT, part = warp / MT;
-  const bool has = tile.adapter < n;
   const int n0 = rank * nslice, n1 = min(N, n0 + nslice);
   int tok[2];  // tokens of the lane's rows, -1: none
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int i = 16 * m + 8 * h + g;
-    const int t = i < tile.rows ? __ldg(perm + tile.row0 + i) : -1;
+    const int t = 8 * h + g < tile.rows ? __ldg(perm + tile.row0 + 8 * h + g) : -1;
     tok[h] = (unsigned)t < (unsigned)T_ ? t : -1;
   }
+  const T* Ba = B + (int64_t)tile.adapter * N * r;
+  {  // B's slice is on its way to L2 while A's is multiplied
+    const int64_t bytes = (int64_t)(n1 - n0) * r * sizeof(T);
+    const char* p = reinterpret_cast<const char*>(Ba + (int64_t)n0 * r);
+    for (int64_t c = threadIdx.x * 128; c < bytes; c += kAdThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+  }
   uint32_t hi[KB][2][4], lo[KB][2][4];
-  const T* Ba = B + (int64_t)(has ? tile.adapter : 0) * N * r;
-  if (has) {
-    if (MT == 1) {  // few tokens: B's slice is on its way to L2 while A's is multiplied
-      const int64_t bytes = (int64_t)(n1 - n0) * r * sizeof(T);
-      const char* p = reinterpret_cast<const char*>(Ba + (int64_t)n0 * r);
-      for (int64_t c = threadIdx.x * 128; c < bytes; c += kAdThreads * 128)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
-    }
+  {
     float acc[NR][4];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
@@ -212,7 +280,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     const T* Ar = A + ((int64_t)tile.adapter * r + g) * K;
     const int k0 = rank * kslice, k1 = min(K, k0 + kslice);
 #pragma unroll 2
-    for (int kk = k0 + part * 32 + q * 8; kk - q * 8 < k1; kk += KG * 32) {
+    for (int kk = k0 + warp * 32 + q * 8; kk - q * 8 < k1; kk += KG * 32) {
       const bool in = kk < k1;  // k1 and kk are multiples of 8
       const uint4 zero = make_uint4(0, 0, 0, 0);
       const uint4 a = in && tok[0] >= 0 ? __ldg(reinterpret_cast<const uint4*>(x0 + kk)) : zero;
@@ -227,56 +295,29 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < NR; ++i) mma16816<T>(acc[i], a1, w[i].z, w[i].w);
     }
-    // the warps' shares, then the blocks', each added in order
-    float* mr = red + part * TM * NR * 8;
+    // the warps' shares added in order, then (gather_p) the blocks'
+    float* mr = red + warp * TM * RP;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < NR; ++i)
-        *reinterpret_cast<float2*>(mr + (16 * m + 8 * h + g) * NR * 8 + 8 * i + 2 * q) =
-            make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
-    __syncthreads();
-    for (int c = threadIdx.x; c < TM * NR * 8; c += kAdThreads) {
-      float s = red[c];
-#pragma unroll
-      for (int p = 1; p < KG; ++p) s += red[p * TM * NR * 8 + c];
-      mine[c] = s;
-    }
-    if (cluster > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    const float sc = __ldg(scale + tile.adapter);
-    for (int c = threadIdx.x; c < TM * RP; c += kAdThreads) {
-      const int row = c / RP, i = c % RP;
-      float s = 0.0f;
-      if (i < r && row < tile.rows) {
-        const float* p = mine + row * NR * 8 + i;
-        if (cluster > 1)
-          for (int b = 0; b < cluster; ++b) s += __uint_as_float(load_remote(p, b));
-        else
-          s = *p;
-        s *= sc;
-      }
-      P[row * LD + i] = s;
-    }
-    if (cluster > 1) cluster_arrive();  // this block has read; it may not leave before the others have
-    __syncthreads();
-    scale_rows<T>(P, LD, RP, TM, undo);
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) split8<T>(P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q, h, hi[b], lo[b]);
+        *reinterpret_cast<float2*>(mr + (8 * h + g) * RP + 8 * i + 2 * q) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
   }
-  float back[2] = {1.0f, 1.0f};
-  if constexpr (is_f16<T>) {
-    if (has)
+  __syncthreads();
+  for (int c = threadIdx.x; c < TM * RP; c += kAdThreads) {
+    float s = red[c];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) back[h] = undo[16 * m + 8 * h + g];
+    for (int p = 1; p < KG; ++p) s += red[p * TM * RP + c];
+    mine[c] = s;
   }
-  for (int nn = n0 + part * 32; nn < n1; nn += KG * 32) {
+  cluster_arrive();
+  cluster_wait();
+  float back[2];
+  gather_p<TM, KB, RP>(mine, cluster, __ldg(scale + tile.adapter), r, tile.rows, P);
+  cluster_arrive();  // this warp has read; no block may leave before all have
+  __syncthreads();
+  operand_p<T, KB>(P, hi, lo, back);
+  for (int nn = n0 + warp * 32; nn < n1; nn += KG * 32) {
     // column c of MMA tile i is output nn + 8*(c/2) + 2*i + c%2, so that a lane ends up
     // with outputs nn + 8q .. nn + 8q + 7 of its rows
     const int col = nn + 8 * q;
@@ -285,35 +326,23 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     for (int h = 0; h < 2; ++h)
       yv[h] = tok[h] >= 0 && col < n1 ? __ldg(reinterpret_cast<const uint4*>(y + (int64_t)tok[h] * ldy + col))
                                       : make_uint4(0, 0, 0, 0);
-    float acc[4][4];
+    float acc[4][4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int b = 0; b < KB; ++b) {
+      uint4 w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-    if (has) {
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        uint4 bv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int o = nn + 8 * (g >> 1) + 2 * i + (g & 1), kk = 32 * b + 8 * q;
-          bv[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk))
-                                   : make_uint4(0, 0, 0, 0);
-        }
-        mma_hi_lo<T>(acc, hi[b], lo[b], bv);
+      for (int i = 0; i < 4; ++i) {
+        const int o = nn + 8 * (g >> 1) + 2 * i + (g & 1), kk = 32 * b + 8 * q;
+        w[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk)) : make_uint4(0, 0, 0, 0);
       }
+      mma_hi_lo<T>(acc, hi[b], lo[b], w);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (tok[h] < 0 || col >= n1) continue;
-      T* o = out + (int64_t)tok[h] * ldo + col;
-      if (has)
-        store_sum<T>(o, yv[h], acc, h, back[h]);
-      else
-        *reinterpret_cast<uint4*>(o) = yv[h];
-    }
+    for (int h = 0; h < 2; ++h)
+      if (tok[h] >= 0 && col < n1) store_sum<T>(out + (int64_t)tok[h] * ldo + col, yv[h], acc, h, back[h]);
   }
-  if (has && cluster > 1) cluster_wait();
+  if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------- long batches
@@ -337,7 +366,7 @@ constexpr int kWideTokens = 64;
 
 template <int NR> constexpr int wide_stage_bytes() { return kWideTokens * 128 + NR * 8 * 128; }
 template <int NR> constexpr int wide_smem_bytes() {
-  return kWideStages * wide_stage_bytes<NR>() + kWideTokens * NR * 8 * 4 + kWideTokens * (NR * 8 + 4) * 4 + kWideTokens * 4;
+  return kWideStages * wide_stage_bytes<NR>() + kWideTokens * (2 * NR * 8 + 4) * 4;
 }
 
 template <typename T, int NR>
@@ -347,16 +376,18 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
                         const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
                         int kslice, int nslice, T* out, int64_t ldo) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  constexpr int TM = kWideTokens, KB = NR / 4, RP = NR * 8, LD = RP + 4, BROW = RP * 2;  // B's row in bytes
+  constexpr int TM = kWideTokens, KB = NR / 4, RP = NR * 8, BROW = RP * 2;  // B's row in bytes
   constexpr int STAGE = wide_stage_bytes<NR>();
   extern __shared__ __align__(128) uint8_t wide_sm[];
   uint8_t* ring = wide_sm;
   float* mine = reinterpret_cast<float*>(ring + kWideStages * STAGE);  // [TM][RP] this block's share of P
-  float* P = mine + TM * RP;                                          // [TM][LD]
-  float* undo = P + TM * LD;                                          // [TM] fp16: takes a row's power of two back
-  const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
-  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, rest);
-  if (tile.rows == 0) return;  // all blocks of the cluster alike
+  float* P = mine + TM * RP;                                          // [TM][KB*32 + 4]
+  const uint32_t rank = cluster_rank();
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_);
+  if (tile.rows == 0) {  // all blocks of the cluster alike
+    if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int m = warp & 3, half = warp >> 2;
   const int k0 = rank * kslice, k1 = min(K, k0 + kslice), n0 = rank * nslice, n1 = min(N, n0 + nslice);
@@ -366,15 +397,6 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   };
   const int chunk = tid & 7, row8 = tid >> 3;  // what the thread copies: 16-byte chunk of rows row8, row8 + 32
   const int src[2] = {token(row8), token(row8 + 32)};
-  if (tile.adapter >= n) {  // rows without an adapter
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (src[h] >= 0)
-        for (int c = n0 + chunk * 8; c < n1; c += 64)
-          *reinterpret_cast<uint4*>(out + (int64_t)src[h] * ldo + c) =
-              __ldg(reinterpret_cast<const uint4*>(y + (int64_t)src[h] * ldy + c));
-    return;
-  }
   const int tok[2] = {token(16 * m + g), token(16 * m + 8 + g)};
   const T* Aa = A + (int64_t)tile.adapter * r * K;
   const T* Ba = B + (int64_t)tile.adapter * N * r;
@@ -421,6 +443,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   };
 #pragma unroll
   for (int st = 0; st < kWideStages - 1; ++st) issue(st);
+  if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
   uint32_t hi[KB][2][4], lo[KB][2][4];
   {
     float acc[NR][4];
@@ -467,48 +490,20 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
           *share(h, i) = make_float2(acc[i][2 * h] + o.x, acc[i][2 * h + 1] + o.y);
         }
   }
-  if (cluster > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  const float sc = __ldg(scale + tile.adapter);
-  for (int c = tid; c < TM * RP; c += kAdThreads) {
-    const int row = c / RP, i = c % RP;
-    float s = 0.0f;
-    if (i < r && row < tile.rows) {
-      const float* p = mine + row * RP + i;
-      if (cluster > 1)
-        for (int b = 0; b < cluster; ++b) s += __uint_as_float(load_remote(p, b));
-      else
-        s = *p;
-      s *= sc;
-    }
-    P[row * LD + i] = s;
-  }
-  if (cluster > 1) cluster_arrive();  // this block has read; it may not leave before the others have
+  cluster_arrive();
+  cluster_wait();
+  float back[2];
+  gather_p<TM, KB, RP>(mine, cluster, __ldg(scale + tile.adapter), r, tile.rows, P);
+  cluster_arrive();  // this warp has read; no block may leave before all have
   __syncthreads();
-  scale_rows<T>(P, LD, RP, TM, undo);
-#pragma unroll
-  for (int b = 0; b < KB; ++b)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) split8<T>(P + (16 * m + 8 * h + g) * LD + 32 * b + 8 * q, h, hi[b], lo[b]);
-  float back[2] = {1.0f, 1.0f};
-  if constexpr (is_f16<T>)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) back[h] = undo[16 * m + 8 * h + g];
+  operand_p<T, KB>(P + 16 * m * (KB * 32 + 4), hi, lo, back);
   for (int st = down; st < down + up; ++st) {
     copy_wait<kWideStages - 2>();
     __syncthreads();
     issue(st + kWideStages - 1);
     const uint8_t* ys = ring + (st & (kWideStages - 1)) * STAGE;
     const uint8_t* bs = ys + TM * 128;
-    float acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    float acc[4][4] = {};
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       uint4 w[4];
@@ -524,7 +519,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     }
   }
   copy_wait<0>();
-  if (cluster > 1) cluster_wait();
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -537,7 +532,7 @@ cudaError_t adapters_with(Kern kern, int TM, int kstep, int smem, const AdapterA
     if (e != cudaSuccess) return e;
   }
   const bool rest = a.out.p != a.y.p;  // rows without an adapter still have to be copied
-  const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM + (rest ? 1 : 0);  // at most this many
+  const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM;  // at most this many
   // as many blocks a tile as fill the machine twice and still have a step of k each
   int cluster = 1;
   while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * kstep) cluster *= 2;
@@ -551,8 +546,8 @@ cudaError_t adapters_with(Kern kern, int TM, int kstep, int smem, const AdapterA
 
 template <typename T, int NR>
 cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
-  constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4) + 16) * (int)sizeof(float);
-  return adapters_with<T>(adapter_kernel<T, NR, 1>, 16, kAdWarps * 32, smem, a, s);
+  constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4)) * (int)sizeof(float);
+  return adapters_with<T>(adapter_kernel<T, NR>, 16, kAdWarps * 32, smem, a, s);
 }
 template <typename T, int NR>
 cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
