@@ -20,6 +20,10 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 
+# the operators' native Python calls (torch's headers and libraries, next to the C ABI library)
+BIND_SRC = os.path.join(HERE, "bind", "ops_bind.cpp")
+BIND_LIB = os.path.join(HERE, "_moe_ops.so")
+
 GEN_SRC = os.path.join(ROOT, "gen", "gen_device.cu")
 GEN_LIB = os.path.join(ROOT, "gen", "libmoegen.so")
 GEN_HOST_SRC = os.path.join(ROOT, "gen", "gen_host.c")
@@ -53,7 +57,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run([NVCC, *ARCH, *FLAGS, "-shared", GEN_SRC, "-o", GEN_LIB + ".tmp"], check=True)
         os.replace(GEN_LIB + ".tmp", GEN_LIB)
     build_gen_host(force)
+    build_bind(force)
     return LIB
+
+
+def build_bind(force: bool = False) -> str:
+    """The operators' native Python calls; loads libmoe_b200.so from its own folder."""
+    if force or _stale(BIND_LIB, [BIND_SRC, os.path.join(ROOT, "include", "moe.h")]):
+        import importlib.util
+        import sysconfig
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        cuda = os.path.dirname(os.path.dirname(NVCC))
+        inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+        subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+                        "-I", os.path.join(ROOT, "include"), *(a for i in inc for a in ("-isystem", i)), BIND_SRC,
+                        "-o", BIND_LIB + ".tmp", "-L", HERE, "-l:libmoe_b200.so", "-Wl,-rpath,$ORIGIN",
+                        "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda",
+                        "-lc10"], check=True)
+        os.replace(BIND_LIB + ".tmp", BIND_LIB)
+    return BIND_LIB
 
 
 def build_gen_host(force: bool = False) -> str:
