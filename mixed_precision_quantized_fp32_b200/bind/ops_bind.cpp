@@ -166,8 +166,8 @@ PyObject* answer(PyObject* given, const at::Tensor& t) {
   return none(given) ? wrap(t) : Py_NewRef(given);
 }
 
-// An 8-bit checkpoint as Python holds it: (memory, offset, exponents or None, R, F).  With
-// exponents None both parts lie in one piece of memory, as save makes it.
+// An 8-bit checkpoint as Python holds it, its handle: (memory, offset, exponents or None,
+// R, F).  With exponents None both parts lie in one piece of memory, as save makes it.
 struct Ckpt {
   int8_t* q;
   uint8_t* e;
@@ -191,6 +191,17 @@ Ckpt ckpt(const Call& c, PyObject* o, int64_t R, int64_t F) {
     refuse("not a checkpoint of [", R, ", ", F, "]: ", shape_of(mem));
   char* p = (char*)mem.data_ptr() + at;
   return {(int8_t*)p, (uint8_t*)p + ckpt_codes(R, F)};
+}
+
+// The handle of the checkpoint at `at` of mem, and its pointers.
+PyObject* new_handle(const at::Tensor& mem, int64_t at, int64_t R, int64_t F, Ckpt* k) {
+  char* p = (char*)mem.data_ptr() + at;
+  *k = {(int8_t*)p, (uint8_t*)p + ckpt_codes(R, F)};
+  return Py_BuildValue("(NLOLL)", wrap(mem), (long long)at, Py_None, (long long)R, (long long)F);
+}
+PyObject* const* pair(PyObject* o) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse("not the checkpoints of g and u");
+  return &PyTuple_GET_ITEM(o, 0);
 }
 
 // ---------------------------------------------------------------- routes
@@ -314,7 +325,7 @@ PyObject* do_collect_backward(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints
-// act_save(x, checkpoint or None, rows, stream): the memory of a new checkpoint, or None
+// act_save(x, handle or None, rows, stream): the handle
 PyObject* do_act_save(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0], "x");
   const Call c(x, a[3]);
@@ -322,17 +333,13 @@ PyObject* do_act_save(PyObject* const* a) {
   if (x.dim() != 2) refuse("x must be a matrix, got ", x.sizes());
   const int32_t R = extent(x.size(0), "R"), F = extent(x.size(1), "F");
   const Rows r = c.rows(x, "x", R, F, x.scalar_type());
-  at::Tensor mem;
   Ckpt k;
-  if (none(a[1])) {
-    mem = c.empty({ckpt_bytes(R, F)}, at::kByte);
-    char* p = (char*)mem.data_ptr();
-    k = {(int8_t*)p, (uint8_t*)p + ckpt_codes(R, F)};
-  } else {
-    k = ckpt(c, a[1], R, F);
-  }
+  const bool fresh = none(a[1]);
+  if (!fresh) k = ckpt(c, a[1], R, F);
+  THPObjectPtr handle(fresh ? new_handle(c.empty({ckpt_bytes(R, F)}, at::kByte), 0, R, F, &k) : Py_NewRef(a[1]));
+  if (!handle) throw Pending{};
   done("moe_act_save", moe_act_save(r.p, r.ld, dt, R, F, k.q, k.e, c.limit(a[2]), c.stream));
-  return mem.defined() ? wrap(mem) : Py_NewRef(Py_None);
+  return handle.release();
 }
 
 // act_load(checkpoint, dtype, x, rows, stream): x
@@ -350,52 +357,54 @@ PyObject* do_act_load(PyObject* const* a) {
   return answer(a[2], x);
 }
 
-// swiglu_save(g, u, h, checkpoint of g, of u, rows, stream): (h, memory of both checkpoints or None)
+// swiglu_save(g, u, h, (handle of g, of u) or None, rows, stream): (h, handles)
 PyObject* do_swiglu_save(PyObject* const* a) {
   const at::Tensor &g = tensor(a[0], "g"), &u = tensor(a[1], "u");
-  const Call c(g, a[6]);
+  const Call c(g, a[5]);
   const int32_t dt = value_type(g, "g");
   if (g.dim() != 2) refuse("g must be a matrix, got ", g.sizes());
   const int32_t R = extent(g.size(0), "R"), F = extent(g.size(1), "F");
   const Rows gr = c.rows(g, "g", R, F, g.scalar_type()), ur = c.rows(u, "u", R, F, g.scalar_type());
   const at::Tensor h = c.given_or_empty(a[2], "h", {R, F}, g.scalar_type());
   const Rows hr = c.rows(h, "h", R, F, g.scalar_type());
-  at::Tensor mem;
   Ckpt kg, ku;
+  PyObject* made;
   if (none(a[3])) {
     const int64_t size = ckpt_bytes(R, F);
-    mem = c.empty({2 * size}, at::kByte);
-    char* p = (char*)mem.data_ptr();
-    kg = {(int8_t*)p, (uint8_t*)p + ckpt_codes(R, F)};
-    ku = {(int8_t*)p + size, (uint8_t*)p + size + ckpt_codes(R, F)};
+    const at::Tensor mem = c.empty({2 * size}, at::kByte);
+    THPObjectPtr first(new_handle(mem, 0, R, F, &kg)), second(new_handle(mem, size, R, F, &ku));
+    made = first && second ? PyTuple_Pack(2, first.get(), second.get()) : nullptr;
   } else {
-    kg = ckpt(c, a[3], R, F);
-    ku = ckpt(c, a[4], R, F);
+    kg = ckpt(c, pair(a[3])[0], R, F);
+    ku = ckpt(c, pair(a[3])[1], R, F);
+    made = Py_NewRef(a[3]);
   }
+  if (!made) throw Pending{};
+  THPObjectPtr handles(made);
   done("moe_swiglu_save", moe_swiglu_save(gr.p, gr.ld, ur.p, ur.ld, dt, R, F, hr.p, hr.ld, kg.q, kg.e, ku.q, ku.e,
-                                          c.limit(a[5]), c.stream));
-  return Py_BuildValue("(NN)", answer(a[2], h), mem.defined() ? wrap(mem) : Py_NewRef(Py_None));
+                                          c.limit(a[4]), c.stream));
+  return Py_BuildValue("(NN)", answer(a[2], h), handles.release());
 }
 
-// swiglu_backward(dh, checkpoint of g, of u, dg, du, h, rebuild_h, rows, stream): (dg, du, h or None)
+// swiglu_backward(dh, (handle of g, of u), dg, du, h, rebuild_h, rows, stream): (dg, du, h or None)
 PyObject* do_swiglu_backward(PyObject* const* a) {
   const at::Tensor& dh = tensor(a[0], "dh");
-  const Call c(dh, a[8]);
+  const Call c(dh, a[7]);
   const int32_t dt = value_type(dh, "dh");
   if (dh.dim() != 2) refuse("dh must be a matrix, got ", dh.sizes());
   const int32_t R = extent(dh.size(0), "R"), F = extent(dh.size(1), "F");
   const auto type = dh.scalar_type();
   const Rows r = c.rows(dh, "dh", R, F, type);
-  const Ckpt kg = ckpt(c, a[1], R, F), ku = ckpt(c, a[2], R, F);
-  const int again = none(a[5]) ? PyObject_IsTrue(a[6]) : 1;
+  const Ckpt kg = ckpt(c, pair(a[1])[0], R, F), ku = ckpt(c, pair(a[1])[1], R, F);
+  const int again = none(a[4]) ? PyObject_IsTrue(a[5]) : 1;
   if (again < 0) throw Pending{};
-  const at::Tensor dg = c.given_or_empty(a[3], "dg", {R, F}, type), du = c.given_or_empty(a[4], "du", {R, F}, type);
-  const at::Tensor h = again ? c.given_or_empty(a[5], "h", {R, F}, type) : at::Tensor();
+  const at::Tensor dg = c.given_or_empty(a[2], "dg", {R, F}, type), du = c.given_or_empty(a[3], "du", {R, F}, type);
+  const at::Tensor h = again ? c.given_or_empty(a[4], "h", {R, F}, type) : at::Tensor();
   const Rows gr = c.rows(dg, "dg", R, F, type), ur = c.rows(du, "du", R, F, type);
   const Rows hr = again ? c.rows(h, "h", R, F, type) : Rows{nullptr, F};
   done("moe_swiglu_backward", moe_swiglu_backward(r.p, r.ld, dt, kg.q, kg.e, ku.q, ku.e, R, F, gr.p, gr.ld, ur.p, ur.ld,
-                                                  hr.p, hr.ld, c.limit(a[7]), c.stream));
-  return Py_BuildValue("(NNN)", answer(a[3], dg), answer(a[4], du), again ? answer(a[5], h) : Py_NewRef(Py_None));
+                                                  hr.p, hr.ld, c.limit(a[6]), c.stream));
+  return Py_BuildValue("(NNN)", answer(a[2], dg), answer(a[3], du), again ? answer(a[4], h) : Py_NewRef(Py_None));
 }
 
 // ---------------------------------------------------------------- adapters
@@ -457,8 +466,8 @@ PyMethodDef methods[] = {{"set_error", set_error, METH_O, nullptr},
                          ENTRY(collect_backward, 9),
                          ENTRY(act_save, 4),
                          ENTRY(act_load, 5),
-                         ENTRY(swiglu_save, 7),
-                         ENTRY(swiglu_backward, 9),
+                         ENTRY(swiglu_save, 6),
+                         ENTRY(swiglu_backward, 8),
                          ENTRY(adapters, 13),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -131,9 +131,9 @@ class ActCkpt:
         return e, e + (R * -(-F // GROUP) + 255) // 256 * 256
 
     @classmethod
-    def _in(cls, mem: torch.Tensor, at: int, R: int, F: int, dtype: torch.dtype) -> "ActCkpt":
+    def _of(cls, handle: tuple, dtype: torch.dtype) -> "ActCkpt":
         k = cls.__new__(cls)
-        k.handle = (mem, at, None, R, F)
+        k.handle = handle
         k.dtype = dtype
         return k
 
@@ -155,33 +155,46 @@ class ActCkpt:
         return mem[at:at + R * G].view(R, G)
 
 
-@dataclass
 class SwigluCkpt:
-    g: ActCkpt
-    u: ActCkpt
+    """What moe_swiglu_backward needs: the checkpoints of g and u."""
+
+    __slots__ = ("handles", "dtype")
+
+    def __init__(self, g: ActCkpt, u: ActCkpt):
+        if g.dtype is not u.dtype:
+            raise ValueError(f"g and u are of one type, got {g.dtype} and {u.dtype}")
+        self.handles = (g.handle, u.handle)
+        self.dtype = g.dtype
+
+    @property
+    def g(self) -> ActCkpt:
+        return ActCkpt._of(self.handles[0], self.dtype)
+
+    @property
+    def u(self) -> ActCkpt:
+        return ActCkpt._of(self.handles[1], self.dtype)
 
 
 def alloc_ckpt(R: int, F: int, dtype: torch.dtype, device=None) -> ActCkpt:
     """Memory for the 8-bit checkpoint of a matrix [R, F] of dtype."""
-    return ActCkpt._in(torch.empty(ActCkpt._bytes(R, F)[1], dtype=torch.uint8, device=device or "cuda"), 0, R, F, dtype)
+    mem = torch.empty(ActCkpt._bytes(R, F)[1], dtype=torch.uint8, device=device or "cuda")
+    return ActCkpt._of((mem, 0, None, R, F), dtype)
 
 
-def _of(ckpt: ActCkpt, t: torch.Tensor) -> tuple:
-    """The checkpoint's handle, for values of t's type."""
+def _same_type(ckpt: ActCkpt | SwigluCkpt, t: torch.Tensor) -> None:
     if ckpt.dtype is not t.dtype:
         raise ValueError(f"the checkpoint is for {ckpt.dtype}, the values are {t.dtype}")
-    return ckpt.handle
 
 
 def moe_act_save(x: torch.Tensor, ckpt: ActCkpt | None = None, rows: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None) -> ActCkpt:
     """x [R, F] kept in 8 bits.  rows: cuda int32 [1], only rows below it are read and
     written (routes.offsets[E:] after a dispatch)."""
-    if ckpt is not None:
-        _moe_ops.act_save(x, _of(ckpt, x), rows, stream)
-        return ckpt
-    mem = _moe_ops.act_save(x, None, rows, stream)
-    return ActCkpt._in(mem, 0, *x.shape, x.dtype)
+    if ckpt is None:
+        return ActCkpt._of(_moe_ops.act_save(x, None, rows, stream), x.dtype)
+    _same_type(ckpt, x)
+    _moe_ops.act_save(x, ckpt.handle, rows, stream)
+    return ckpt
 
 
 def moe_act_load(ckpt: ActCkpt, x: torch.Tensor | None = None, rows: torch.Tensor | None = None,
@@ -194,11 +207,13 @@ def moe_swiglu_save(g: torch.Tensor, u: torch.Tensor, h: torch.Tensor | None = N
                     rows: torch.Tensor | None = None,
                     stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, SwigluCkpt]:
     """h = silu(g) * u and the 8-bit checkpoint of g and u that moe_swiglu_backward needs."""
-    if ckpt is not None:
-        return _moe_ops.swiglu_save(g, u, h, _of(ckpt.g, g), _of(ckpt.u, u), rows, stream)[0], ckpt
-    h, mem = _moe_ops.swiglu_save(g, u, h, None, None, rows, stream)
-    R, F = g.shape
-    return h, SwigluCkpt(ActCkpt._in(mem, 0, R, F, g.dtype), ActCkpt._in(mem, ActCkpt._bytes(R, F)[1], R, F, g.dtype))
+    if ckpt is None:
+        ckpt = SwigluCkpt.__new__(SwigluCkpt)
+        h, ckpt.handles = _moe_ops.swiglu_save(g, u, h, None, rows, stream)
+        ckpt.dtype = g.dtype
+        return h, ckpt
+    _same_type(ckpt, g)
+    return _moe_ops.swiglu_save(g, u, h, ckpt.handles, rows, stream)[0], ckpt
 
 
 def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | None = None,
@@ -207,7 +222,7 @@ def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | N
                         ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor | None]:
     """(dg, du, h) from dh and the checkpoint, all of dh's type; h, the activation again, only
     if it is given or rebuild_h is set."""
-    return _moe_ops.swiglu_backward(dh, ckpt.g.handle, ckpt.u.handle, dg, du, h, rebuild_h, rows, stream)
+    return _moe_ops.swiglu_backward(dh, ckpt.handles, dg, du, h, rebuild_h, rows, stream)
 
 
 # ------------------------------------------------------------------ adapters
