@@ -54,13 +54,17 @@ struct Tile {
 };
 
 // Tile `want` of the sorted rows: each adapter's rows in tiles of TM, adapters in order.
-// Every thread takes a run of adapters and the block scans their tile counts.
-__device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets, int n, int T) {
+// Every thread takes a run of adapters and the block scans their tile counts.  first: shared
+// memory for the first kAdThreads entries of perm, which short batches take from there, so
+// that they are loaded together with the offsets and not after them.
+__device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets, int n, int T,
+                          const int32_t* __restrict__ perm, int32_t* first) {
   __shared__ int wsum[kAdWarps];
   __shared__ Tile found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + kAdThreads - 1) / kAdThreads;
   if (tid == 0) found = {0, 0, 0};
+  const int mine_of_perm = first && tid < T ? __ldg(perm + tid) : -1;
   auto lo_of = [&](int a) { return min(max(__ldg(offsets + a), 0), T); };
   auto hi_of = [&](int a, int lo) { return min(max(__ldg(offsets + a + 1), lo), T); };
   int mine = 0;
@@ -77,6 +81,7 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
     if (lane >= o) s += u;
   }
   if (lane == 31) wsum[warp] = s;
+  if (first) first[tid] = mine_of_perm;
   __syncthreads();
   int before = s - mine;
   for (int w = 0; w < warp; ++w) before += wsum[w];
@@ -97,27 +102,28 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
   return found;
 }
 
-// out = y for the rows without an adapter, those behind the last adapter's: a share of them
-// for every warp, whether its block has a tile or not, eight pieces of a row in flight.
+// out = y for the rows without an adapter, those from `first` on: a share of them for every
+// warp, whether its block has a tile or not.  The shares, 128 pieces of 16 bytes, start at the
+// last blocks, which have no tile if any has none.
 template <typename T>
-__device__ void copy_rest(const T* y, int64_t ldy, T* out, int64_t ldo, int N, int n, int T_,
-                          const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets) {
-  const int lane = threadIdx.x & 31, first = min(max(__ldg(offsets + n), 0), T_);
-  const int block = gridDim.x - 1 - blockIdx.x;  // the last blocks have no tile, if any
-  for (int row = first + block * kAdWarps + (threadIdx.x >> 5); row < T_; row += gridDim.x * kAdWarps) {
-    const int t = __ldg(perm + row);
+__device__ void copy_rest(const T* y, int64_t ldy, T* out, int64_t ldo, int N, int first, int T_,
+                          const int32_t* __restrict__ perm) {
+  const int lane = threadIdx.x & 31, pieces = N / 8, shares = (pieces + 127) / 128;
+  const int64_t all = (int64_t)(T_ - first) * shares;
+  for (int64_t i = (int64_t)(gridDim.x - 1 - blockIdx.x) * kAdWarps + (threadIdx.x >> 5); i < all;
+       i += (int64_t)gridDim.x * kAdWarps) {
+    const int row = (int)(i / shares), t = __ldg(perm + first + row);
     if ((unsigned)t >= (unsigned)T_) continue;
-    const uint4* from = reinterpret_cast<const uint4*>(y + (int64_t)t * ldy);
-    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)t * ldo);
-    for (int c = lane; c < N / 8; c += 256) {
-      uint4 v[8];
+    const int c0 = (int)(i - (int64_t)row * shares) * 128 + lane;
+    const uint4* from = reinterpret_cast<const uint4*>(y + (int64_t)t * ldy) + c0;
+    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)t * ldo) + c0;
+    uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + 32 * i < N / 8) v[i] = __ldg(from + c + 32 * i);
+    for (int k = 0; k < 4; ++k)
+      if (c0 + 32 * k < pieces) v[k] = __ldg(from + 32 * k);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + 32 * i < N / 8) to[c + 32 * i] = v[i];
-    }
+    for (int k = 0; k < 4; ++k)
+      if (c0 + 32 * k < pieces) to[32 * k] = v[k];
   }
 }
 
@@ -247,18 +253,23 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   float* red = sm;                  // [KG][TM][RP] shares of the warps
   float* mine = red + KG * TM * RP;  // [TM][RP] this block's share of P
   float* P = mine + TM * RP;         // [TM][KB*32 + 4]
+  __shared__ int32_t first[kAdThreads];
   const uint32_t rank = cluster_rank();
-  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_);
+  const int rest0 = rest ? min(max(__ldg(offsets + n), 0), T_) : T_;
+  const bool few = T_ <= kAdThreads;
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, perm, few ? first : nullptr);
   if (tile.rows == 0) {  // all blocks of the cluster alike
-    if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+    if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
     return;
   }
+  const float sc = __ldg(scale + tile.adapter);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int n0 = rank * nslice, n1 = min(N, n0 + nslice);
   int tok[2];  // tokens of the lane's rows, -1: none
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int t = 8 * h + g < tile.rows ? __ldg(perm + tile.row0 + 8 * h + g) : -1;
+    const int row = tile.row0 + 8 * h + g;
+    const int t = 8 * h + g >= tile.rows ? -1 : few ? first[row] : __ldg(perm + row);
     tok[h] = (unsigned)t < (unsigned)T_ ? t : -1;
   }
   const T* Ba = B + (int64_t)tile.adapter * N * r;
@@ -311,37 +322,53 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     mine[c] = s;
   }
   cluster_arrive();
+  // column c of MMA tile i is output nn + 8*(c/2) + 2*i + c%2, so that a lane ends up with
+  // outputs nn + 8q .. nn + 8q + 7 of its rows
+  auto load_y = [&](int nn, uint4 (&v)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = tok[h] >= 0 && nn + 8 * q < n1
+                 ? __ldg(reinterpret_cast<const uint4*>(y + (int64_t)tok[h] * ldy + nn + 8 * q))
+                 : make_uint4(0, 0, 0, 0);
+  };
+  auto load_b = [&](int nn, int b, uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int o = nn + 8 * (g >> 1) + 2 * i + (g & 1), kk = 32 * b + 8 * q;
+      v[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // the first step's operands are on their way while the cluster meets (of B the first 32 or 64 of the rank)
+  constexpr int AHEAD = KB < 2 ? KB : 2;
+  int nn = n0 + warp * 32;
+  uint4 yv[2], bv[AHEAD][4];
+  load_y(nn, yv);
+#pragma unroll
+  for (int b = 0; b < AHEAD; ++b) load_b(nn, b, bv[b]);
   cluster_wait();
   float back[2];
-  gather_p<TM, KB, RP>(mine, cluster, __ldg(scale + tile.adapter), r, tile.rows, P);
+  gather_p<TM, KB, RP>(mine, cluster, sc, r, tile.rows, P);
   cluster_arrive();  // this warp has read; no block may leave before all have
   __syncthreads();
   operand_p<T, KB>(P, hi, lo, back);
-  for (int nn = n0 + warp * 32; nn < n1; nn += KG * 32) {
-    // column c of MMA tile i is output nn + 8*(c/2) + 2*i + c%2, so that a lane ends up
-    // with outputs nn + 8q .. nn + 8q + 7 of its rows
-    const int col = nn + 8 * q;
-    uint4 yv[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      yv[h] = tok[h] >= 0 && col < n1 ? __ldg(reinterpret_cast<const uint4*>(y + (int64_t)tok[h] * ldy + col))
-                                      : make_uint4(0, 0, 0, 0);
+  while (nn < n1) {
     float acc[4][4] = {};
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      uint4 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int o = nn + 8 * (g >> 1) + 2 * i + (g & 1), kk = 32 * b + 8 * q;
-        w[i] = o < n1 && kk < r ? __ldg(reinterpret_cast<const uint4*>(Ba + (int64_t)o * r + kk)) : make_uint4(0, 0, 0, 0);
-      }
-      mma_hi_lo<T>(acc, hi[b], lo[b], w);
+      if (b >= AHEAD) load_b(nn, b, bv[b % AHEAD]);
+      mma_hi_lo<T>(acc, hi[b], lo[b], bv[b % AHEAD]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (tok[h] >= 0 && col < n1) store_sum<T>(out + (int64_t)tok[h] * ldo + col, yv[h], acc, h, back[h]);
+      if (tok[h] >= 0 && nn + 8 * q < n1)
+        store_sum<T>(out + (int64_t)tok[h] * ldo + nn + 8 * q, yv[h], acc, h, back[h]);
+    nn += KG * 32;
+    if (nn >= n1) break;
+    load_y(nn, yv);
+#pragma unroll
+    for (int b = 0; b < AHEAD; ++b) load_b(nn, b, bv[b]);
   }
-  if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+  if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
   cluster_wait();
 }
 
@@ -383,11 +410,13 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   float* mine = reinterpret_cast<float*>(ring + kWideStages * STAGE);  // [TM][RP] this block's share of P
   float* P = mine + TM * RP;                                          // [TM][KB*32 + 4]
   const uint32_t rank = cluster_rank();
-  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_);
+  const int rest0 = rest ? min(max(__ldg(offsets + n), 0), T_) : T_;
+  const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, perm, nullptr);
   if (tile.rows == 0) {  // all blocks of the cluster alike
-    if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+    if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
     return;
   }
+  const float sc = __ldg(scale + tile.adapter);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int m = warp & 3, half = warp >> 2;
   const int k0 = rank * kslice, k1 = min(K, k0 + kslice), n0 = rank * nslice, n1 = min(N, n0 + nslice);
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   };
 #pragma unroll
   for (int st = 0; st < kWideStages - 1; ++st) issue(st);
-  if (rest) copy_rest(y, ldy, out, ldo, N, n, T_, perm, offsets);
+  if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
   uint32_t hi[KB][2][4], lo[KB][2][4];
   {
     float acc[NR][4];
@@ -493,7 +522,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   cluster_arrive();
   cluster_wait();
   float back[2];
-  gather_p<TM, KB, RP>(mine, cluster, __ldg(scale + tile.adapter), r, tile.rows, P);
+  gather_p<TM, KB, RP>(mine, cluster, sc, r, tile.rows, P);
   cluster_arrive();  // this warp has read; no block may leave before all have
   __syncthreads();
   operand_p<T, KB>(P + 16 * m * (KB * 32 + 4), hi, lo, back);
@@ -533,9 +562,9 @@ cudaError_t adapters_with(Kern kern, int TM, int kstep, int smem, const AdapterA
   }
   const bool rest = a.out.p != a.y.p;  // rows without an adapter still have to be copied
   const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM;  // at most this many
-  // as many blocks a tile as fill the machine twice and still have a step of k each
+  // as many blocks a tile as the machine holds at once and still have a step of k each
   int cluster = 1;
-  while (cluster < kAdMaxCluster && tiles * cluster < 2 * 148 && a.K > cluster * kstep) cluster *= 2;
+  while (cluster < kAdMaxCluster && 2 * tiles * cluster <= 3 * 148 && a.K > cluster * kstep) cluster *= 2;
   const int kslice = ((a.K + cluster - 1) / cluster + 31) / 32 * 32;
   const int nslice = ((a.N + cluster - 1) / cluster + 31) / 32 * 32;
   return launch_cluster(kern, dim3((unsigned)tiles * cluster), dim3(kAdThreads), cluster, smem, stream,
