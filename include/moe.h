@@ -473,6 +473,8 @@ MOE_API moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t dty
  * scale: DEVICE fp32 [n].
  * perm, offsets: moe_sort of the tokens' adapters (k = 1, E = n, -1: none); one sort
  *   serves every layer of a step.  An entry of perm outside [0, T) is skipped.
+ * status: DEVICE i32 [1] or NULL: MOE_ERR_TIMEOUT is written there if a bounded wait of the
+ *   kernel gave up (out is undefined then); nothing is written otherwise.
  * Limits: T <= 2^20; 1 <= n <= MOE_MAX_GROUPS; r a multiple of 8 up to 128; K and N
  *   multiples of 8 from 8 to 2^20.  All matrices 16-byte aligned, pitches multiples of
  *   8 values (MOE_ERR_ALIGN).
@@ -480,7 +482,7 @@ MOE_API moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t dty
 MOE_API moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
                                 int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
                                 const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
-                                int64_t ldo, cudaStream_t stream);
+                                int64_t ldo, int32_t* status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -82,7 +82,7 @@ def load() -> C.CDLL:
             "moe_act_load": [P, P, i32, i32, i32, P, i64, P, P],
             "moe_swiglu_save": [P, i64, P, i64, i32, i32, i32, P, i64, P, P, P, P, P, P],
             "moe_swiglu_backward": [P, i64, i32, P, P, P, P, i32, i32, P, i64, P, i64, P, i64, P, P],
-            "moe_adapters": [P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, i64, P],
+            "moe_adapters": [P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, i64, P, P],
         }.items():
             fn = getattr(L, name)
             fn.restype, fn.argtypes = C.c_int, args

@@ -408,10 +408,10 @@ PyObject* do_swiglu_backward(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------- adapters
-// adapters(x, y, A, B, scale, perm, inv, offsets, T, k, E, out, stream): out
+// adapters(x, y, A, B, scale, perm, inv, offsets, T, k, E, out, status, stream): out
 PyObject* do_adapters(PyObject* const* a) {
   const at::Tensor &x = tensor(a[0], "x"), &y = tensor(a[1], "y"), &A = tensor(a[2], "A"), &B = tensor(a[3], "B");
-  const Call c(x, a[12]);
+  const Call c(x, a[13]);
   const int32_t dt = value_type(x, "x");
   const auto type = x.scalar_type();
   if (x.dim() != 2) refuse("x must be a matrix, got ", x.sizes());
@@ -427,8 +427,9 @@ PyObject* do_adapters(PyObject* const* a) {
   const Routes rt = routes(c, a[5], a[6], a[7], T, n);
   const at::Tensor out = c.given_or_empty(a[11], "out", {T, N}, type);
   const Rows outr = c.rows(out, "out", T, N, type);
+  int32_t* status = none(a[12]) ? nullptr : (int32_t*)c.flat(a[12], "status", 1, at::kInt);
   done("moe_adapters", moe_adapters(xr.p, xr.ld, yr.p, yr.ld, dt, T, K, N, r, n, Ap, Bp, scale, rt.perm, rt.offsets, outr.p,
-                                    outr.ld, c.stream));
+                                    outr.ld, status, c.stream));
   return answer(a[11], out);
 }
 
@@ -468,7 +469,7 @@ PyMethodDef methods[] = {{"set_error", set_error, METH_O, nullptr},
                          ENTRY(act_load, 5),
                          ENTRY(swiglu_save, 6),
                          ENTRY(swiglu_backward, 8),
-                         ENTRY(adapters, 13),
+                         ENTRY(adapters, 14),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -19,12 +19,14 @@
 // stays far below that of the stored result; in fp16 a row is first brought to at most
 // 2^14 by a power of two, since P may pass fp16's range.
 #include "ops_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
 constexpr int kAdWarps = 8;
 constexpr int kAdThreads = 32 * kAdWarps;
 constexpr int kAdMaxCluster = 8;
+constexpr long long kWideWait = 2000000000ll;  // cycles a wait on the tensor cores may take, about a second
 #ifndef XSHORT
 #define XSHORT 128
 #define XPER 16
@@ -373,27 +375,68 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
 }
 
 // ---------------------------------------------------------------- long batches
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {  // zeros where `in` is false
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-               "r"(in ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {  // zeros where `in` is false
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// 16 tensor-memory lanes x 8*X 32-bit columns: lane (g, q) of the warp gets, for every 8
+// columns, columns 2q and 2q + 1 of row g, then of row g + 8 (an m16n8 accumulator).
+template <int X>
+__device__ __forceinline__ void tmem_rows16(uint32_t taddr, float (&r)[X][4]) {
+  static_assert(X == 2 || X == 4 || X == 8, "");
+  float* f = &r[0][0];
+  if constexpr (X == 2)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "r"(taddr));
+  else if constexpr (X == 4)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]),
+          "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
+        : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]),
+          "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15]), "=f"(f[16]),
+          "=f"(f[17]), "=f"(f[18]), "=f"(f[19]), "=f"(f[20]), "=f"(f[21]), "=f"(f[22]), "=f"(f[23]), "=f"(f[24]),
+          "=f"(f[25]), "=f"(f[26]), "=f"(f[27]), "=f"(f[28]), "=f"(f[29]), "=f"(f[30]), "=f"(f[31])
+        : "r"(taddr));
+}
+
 // Tiles of 64 tokens of one adapter.  The same two products and the same split over a
-// cluster, but operands come through a ring of 64-wide stages in shared memory (x and A,
-// then y and B, one ring over both products), since a tile's loads no longer fit in
-// registers ahead of their use.  Warps: 4 token tiles times 2 halves of a stage.
-// Rows of a stage are 128 bytes (B's: the rank); a lane reads the 16 bytes at chunk q of
-// its half in row g, and odd rows have their halves swapped, so the eight lanes of a
-// phase hit eight different 16-byte columns.
+// cluster, on tcgen05 with accumulators in tensor memory: at ranks of 64 the mma.sync form
+// spent half its time feeding and running the tensor cores beside the loads.  Operands come
+// through one ring of 64-wide stages in shared memory over both products: x and A, then y and
+// B.  All threads copy (cp.async: tokens are gathered, so there is no box for a TMA load);
+// one warp issues each stage's MMAs, whose completion frees the stage.
+//   D1[64][RP]  = sum over k of x A^T        tensor memory columns 0 .. 127
+//   D2[64][64]  = P_lo B^T + P_hi B^T        two buffers, columns 128 .. 255; one is drained
+//                                            and added to y while the next is computed
+// x, A, B and P lie in 128-byte swizzled rows (16-byte chunk c of row j at c ^ (j % 8)), as the
+// matrix descriptors say.  Row j of a B stage is output 8*(c/2) + 2*i + c%2 of its half of the
+// 64, with i = j/8 % 4 and c = j % 8, so that a lane of the epilogue has eight outputs in a row.
+// Two blocks share an SM; each asks for 256 of its 512 tensor-memory columns and for more than
+// a third of its shared memory, so that a third block never waits for columns.
 constexpr int kWideStages = 4;
 constexpr int kWideTokens = 64;
+constexpr uint32_t kWideTmem = 256;
+constexpr int kWideTile = 64 * 128;  // 64 rows of 128 bytes
 
-template <int NR> constexpr int wide_stage_bytes() { return kWideTokens * 128 + NR * 8 * 128; }
+template <int NR> constexpr int wide_stage_bytes() { return kWideTile + (NR <= 8 ? kWideTile : 2 * kWideTile); }
 template <int NR> constexpr int wide_smem_bytes() {
-  return kWideStages * wide_stage_bytes<NR>() + kWideTokens * (2 * NR * 8 + 4) * 4;
+  const int need = 1024 + kWideStages * wide_stage_bytes<NR>() + 2 * (NR <= 8 ? 1 : 2) * kWideTile +
+                   kWideTokens * NR * 8 * 4 + kWideTokens * 4;
+  return need < 80 * 1024 ? 80 * 1024 : need;
+}
+
+template <typename T> __host__ __device__ constexpr uint32_t wide_idesc(int N) {
+  const uint32_t type = is_f16<T> ? 0u : 1u;  // of A and of B
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kWideTokens >> 4) << 24);
 }
 
 template <typename T, int NR>
@@ -401,14 +444,18 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     adapter_wide_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r,
                         int n, const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
                         const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
-                        int kslice, int nslice, T* out, int64_t ldo) {
+                        int kslice, int nslice, T* out, int64_t ldo, int32_t* status) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  constexpr int TM = kWideTokens, KB = NR / 4, RP = NR * 8, BROW = RP * 2;  // B's row in bytes
+  constexpr int TM = kWideTokens, RP = NR * 8, KBLK = NR <= 8 ? 1 : 2, HALF = RP / 16;  // HALF: n8 tiles of half of P
   constexpr int STAGE = wide_stage_bytes<NR>();
-  extern __shared__ __align__(128) uint8_t wide_sm[];
-  uint8_t* ring = wide_sm;
-  float* mine = reinterpret_cast<float*>(ring + kWideStages * STAGE);  // [TM][RP] this block's share of P
-  float* P = mine + TM * RP;                                          // [TM][KB*32 + 4]
+  extern __shared__ uint8_t wide_sm[];
+  __shared__ uint64_t done[kWideStages];  // the MMAs that read a stage have completed
+  __shared__ uint32_t tmem_at;
+  __shared__ int given_up;
+  const uint32_t ring = (ptx::smem_u32(wide_sm) + 1023u) & ~1023u;  // swizzled tiles start at multiples of 1024
+  const uint32_t p_hi = ring + kWideStages * STAGE, p_lo = p_hi + KBLK * kWideTile;
+  float* mine = reinterpret_cast<float*>(wide_sm + (p_lo + KBLK * kWideTile - ptx::smem_u32(wide_sm)));  // [TM][RP]
+  float* undo = mine + TM * RP;  // [TM] fp16: what takes a row's power of two back
   const uint32_t rank = cluster_rank();
   const int rest0 = rest ? min(max(__ldg(offsets + n), 0), T_) : T_;
   const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, perm, nullptr);
@@ -418,7 +465,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   }
   const float sc = __ldg(scale + tile.adapter);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int m = warp & 3, half = warp >> 2;
+  const int m = warp & 3, half = warp >> 2;  // a warp reads 16 tokens' lanes of tensor memory, half of the columns
   const int k0 = rank * kslice, k1 = min(K, k0 + kslice), n0 = rank * nslice, n1 = min(N, n0 + nslice);
   auto token = [&](int row) {
     const int t = row < tile.rows ? __ldg(perm + tile.row0 + row) : -1;
@@ -430,157 +477,229 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   const T* Aa = A + (int64_t)tile.adapter * r * K;
   const T* Ba = B + (int64_t)tile.adapter * N * r;
   const int down = k1 > k0 ? (k1 - k0 + 63) / 64 : 0, up = n1 > n0 ? (n1 - n0 + 63) / 64 : 0;
+  auto swizzled = [](uint32_t tile_at, int row, int c) { return tile_at + row * 128 + ((c ^ (row & 7)) << 4); };
+  auto stage_at = [&](int st) { return ring + (st & (kWideStages - 1)) * STAGE; };
   auto issue = [&](int st) {
-    uint8_t* base = ring + (st & (kWideStages - 1)) * STAGE;
+    const uint32_t base = stage_at(st), second = base + kWideTile;
     if (st < down) {
       const int k = k0 + st * 64 + chunk * 8;
       const bool in = k < k1;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = row8 + 32 * h;
-        copy16(base + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), src[h] >= 0 ? x + (int64_t)src[h] * ldx + (in ? k : 0) : x,
-               in && src[h] >= 0);
+        const bool real = in && src[h] >= 0;
+        copy16(swizzled(base, row8 + 32 * h, chunk), real ? x + (int64_t)src[h] * ldx + k : x, real);
       }
 #pragma unroll
       for (int j = 0; j < NR / 4; ++j) {
         const int row = row8 + 32 * j;
         const bool real = in && row < r;
-        copy16(base + TM * 128 + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), real ? Aa + (int64_t)row * K + k : Aa, real);
+        copy16(swizzled(second, row, chunk), real ? Aa + (int64_t)row * K + k : Aa, real);
       }
     } else if (st < down + up) {
       const int c0 = n0 + (st - down) * 64, c = c0 + chunk * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = row8 + 32 * h;
-        const bool in = c < n1 && src[h] >= 0;
-        copy16(base + row * 128 + ((chunk ^ ((row & 1) * 4)) * 16), in ? y + (int64_t)src[h] * ldy + c : y, in);
+        const bool real = c < n1 && src[h] >= 0;
+        copy16(swizzled(base, row8 + 32 * h, chunk), real ? y + (int64_t)src[h] * ldy + c : y, real);
       }
-      // NR chunks a row: NR/4 a thread
 #pragma unroll
-      for (int j = 0; j < NR / 4; ++j) {
-        const int i = tid + kAdThreads * j, row = i / NR, b = i % NR;
-        const bool in = c0 + row < n1 && b * 8 < r;
-        copy16(base + TM * 128 + row * BROW + ((NR >= 8 ? b ^ ((row & 1) * 4) : b) * 16),
-               in ? Ba + (int64_t)(c0 + row) * r + b * 8 : Ba, in);
+      for (int j = 0; j < NR / 4; ++j) {  // NR chunks a row
+        const int i = tid + kAdThreads * j, o = i / NR, b = i % NR;
+        const bool real = c0 + o < n1 && b * 8 < r;
+        const int row = (o & 32) + ((o >> 1) & 3) * 8 + ((o >> 3) & 3) * 2 + (o & 1);
+        copy16(swizzled(second + (b >> 3) * kWideTile, row, b & 7), real ? Ba + (int64_t)(c0 + o) * r + b * 8 : Ba, real);
       }
     }
     copy_commit();
   };
-  // 16 bytes at chunk c of row `row` of a tile with `pitch` bytes a row
-  auto piece = [](const uint8_t* base, int row, int c, int pitch) {
-    return *reinterpret_cast<const uint4*>(base + row * pitch + ((pitch >= 128 ? c ^ ((row & 1) * 4) : c) * 16));
+  auto wait_done = [&](int st) {  // of the stage's MMAs; bounded
+    if (!ptx::mbar_wait(&done[st & (kWideStages - 1)], (st >> 2) & 1, &given_up, kWideWait)) given_up = 1;
   };
 #pragma unroll
   for (int st = 0; st < kWideStages - 1; ++st) issue(st);
+  if (warp == 0) {
+    ptx::tmem_alloc(&tmem_at, kWideTmem);
+    ptx::tmem_relinquish();  // at once: the SM's other block waits for the permit
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kWideStages; ++i) ptx::mbar_init(&done[i], 1);
+    ptx::fence_mbar_init();
+    given_up = 0;
+  }
   if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
-  uint32_t hi[KB][2][4], lo[KB][2][4];
-  {
-    float acc[NR][4];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-    for (int st = 0; st < down; ++st) {
-      copy_wait<kWideStages - 2>();
-      __syncthreads();
-      issue(st + kWideStages - 1);
-      const uint8_t* xs = ring + (st & (kWideStages - 1)) * STAGE;
-      const uint8_t* as = xs + TM * 128;
-      const uint4 a = piece(xs, 16 * m + g, 4 * half + q, 128), b = piece(xs, 16 * m + 8 + g, 4 * half + q, 128);
-      const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
-      constexpr int PART = NR < 8 ? NR : 8;  // independent sums between two that depend on one another
-#pragma unroll
-      for (int i0 = 0; i0 < NR; i0 += PART) {
-        uint4 w[PART];
-#pragma unroll
-        for (int i = 0; i < PART; ++i) w[i] = piece(as, 8 * (i0 + i) + g, 4 * half + q, 128);
-#pragma unroll
-        for (int i = 0; i < PART; ++i) mma16816<T>(acc[i0 + i], a0, w[i].x, w[i].y);
-#pragma unroll
-        for (int i = 0; i < PART; ++i) mma16816<T>(acc[i0 + i], a1, w[i].z, w[i].w);
-      }
-    }
-    // the two halves, then the blocks, each added in order
-    auto share = [&](int h, int i) {
-      return reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * RP + 8 * i + 2 * q);
-    };
-    if (half == 1)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < NR; ++i) *share(h, i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_at, my_lanes = (uint32_t)(m * 32) << 16;
+  for (int st = 0; st < down; ++st) {
+    copy_wait<kWideStages - 2>();
+    ptx::fence_proxy_async_smem();
     __syncthreads();
-    if (half == 0)
+    if (warp == 0) {
+      const uint64_t xd = ptx::sw128_desc(stage_at(st)), ad = ptx::sw128_desc(stage_at(st) + kWideTile);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int k = 0; k < 4; ++k)  // 16 values, 32 bytes, at a time
+        ptx::mma_f16_ss_warp(tmem, xd + 2 * k, ad + 2 * k, wide_idesc<T>(RP), st || k ? 1u : 0u);
+      ptx::mma_commit_warp(&done[st & (kWideStages - 1)]);
+    }
+    if (st > 0) wait_done(st - 1);
+    issue(st + kWideStages - 1);
+  }
+  {  // this block's share of P; a block without k values has zeros
+    float acc[HALF][4] = {};
+    if (down > 0) {
+      wait_done(down - 1);
+      ptx::tc_fence_after();
+      tmem_rows16<HALF>(tmem + my_lanes + half * (RP / 2), acc);
+      ptx::tmem_ld_wait();
+    }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const float2 o = *share(h, i);
-          *share(h, i) = make_float2(acc[i][2 * h] + o.x, acc[i][2 * h + 1] + o.y);
-        }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < HALF; ++i)
+        *reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * RP + half * (RP / 2) + 8 * i + 2 * q) =
+            make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
   }
   cluster_arrive();
   cluster_wait();
-  float back[2];
-  gather_p<TM, KB, RP>(mine, cluster, sc, r, tile.rows, P);
-  cluster_arrive();  // this warp has read; no block may leave before all have
-  __syncthreads();
-  operand_p<T, KB>(P + 16 * m * (KB * 32 + 4), hi, lo, back);
-  for (int st = down; st < down + up; ++st) {
-    copy_wait<kWideStages - 2>();
-    __syncthreads();
-    issue(st + kWideStages - 1);
-    const uint8_t* ys = ring + (st & (kWideStages - 1)) * STAGE;
-    const uint8_t* bs = ys + TM * 128;
-    float acc[4][4] = {};
+  // P: the blocks' shares added in order, in 16-byte pieces, and split into hi and lo terms
+  constexpr int PIECES = RP / 4;  // lanes of a row, a power of two up to 32
+#pragma unroll 2
+  for (int c = tid; c < TM * PIECES; c += kAdThreads) {
+    const int row = c / PIECES, piece = c % PIECES;
+    float4 s = make_float4(0, 0, 0, 0);
+    if (piece * 4 < r && row < tile.rows) {  // the rank is a multiple of 8
+      float4 v[kAdMaxCluster];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      uint4 w[4];
+      for (int k = 0; k < kAdMaxCluster; ++k)
+        if (k < cluster) v[k] = load_remote4(mine + c * 4, k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = piece(bs, 32 * half + 8 * (g >> 1) + 2 * i + (g & 1), 4 * b + q, BROW);
-      mma_hi_lo<T>(acc, hi[b], lo[b], w);
+      for (int k = 0; k < kAdMaxCluster; ++k)
+        if (k < cluster) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+      s.x *= sc, s.y *= sc, s.z *= sc, s.w *= sc;
     }
-    const int col = n0 + (st - down) * 64 + 32 * half + 8 * q;
+    if constexpr (is_f16<T>) {  // the row's lanes agree on its power of two
+      uint32_t big = max(max(__float_as_uint(s.x) & 0x7FFFFFFFu, __float_as_uint(s.y) & 0x7FFFFFFFu),
+                         max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (tok[h] < 0 || col >= n1) continue;
-      store_sum<T>(out + (int64_t)tok[h] * ldo + col, piece(ys, 16 * m + 8 * h + g, 4 * half + q, 128), acc, h, back[h]);
+      for (int o = PIECES / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
+      const bool scaled = big < 0x7F800000u && e > 0;
+      const float by = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
+      s.x *= by, s.y *= by, s.z *= by, s.w *= by;
+      if (piece == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+    }
+    uint32_t hi[2], lo[2];
+    split2<T>(s.x, s.y, hi[0], lo[0]);
+    split2<T>(s.z, s.w, hi[1], lo[1]);
+    const uint32_t at = swizzled((piece >> 4) * kWideTile, row, (piece & 15) >> 1) + (piece & 1) * 8;
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_hi + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_lo + at), "r"(lo[0]), "r"(lo[1]) : "memory");
+  }
+  cluster_arrive();  // this warp has read; no block may leave before all have
+  for (int st = down; st < down + up + 1; ++st) {
+    if (st < down + up) {
+      copy_wait<kWideStages - 2>();
+      ptx::fence_proxy_async_smem();  // the first time of P's terms too
+      __syncthreads();
+      if (warp == 0) {
+        ptx::tc_fence_after();
+        const uint32_t d2 = tmem + 128 + (st & 1) * 64;
+        const uint64_t bd = ptx::sw128_desc(stage_at(st) + kWideTile);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {  // small terms first
+          const uint64_t pd = ptx::sw128_desc(term == 0 ? p_lo : p_hi);
+#pragma unroll
+          for (int k = 0; k < RP / 16; ++k) {
+            const uint64_t at = (uint64_t)((k >> 2) * (kWideTile >> 4) + (k & 3) * 2);
+            ptx::mma_f16_ss_warp(d2, pd + at, bd + at, wide_idesc<T>(64), term || k ? 1u : 0u);
+          }
+        }
+        ptx::mma_commit_warp(&done[st & (kWideStages - 1)]);
+      }
+    }
+    if (st > down) {  // y + what the stage before came to
+      const int was = st - 1, col = n0 + (was - down) * 64 + 32 * half + 8 * q;
+      wait_done(was);
+      ptx::tc_fence_after();
+      float acc[4][4];
+      tmem_rows16<4>(tmem + my_lanes + 128 + (was & 1) * 64 + 32 * half, acc);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (tok[h] < 0 || col >= n1) continue;
+        const int row = 16 * m + 8 * h + g;
+        store_sum<T>(out + (int64_t)tok[h] * ldo + col, ptx::lds_v4(swizzled(stage_at(was), row, 4 * half + q)), acc, h,
+                     is_f16<T> ? undo[row] : 1.0f);
+      }
+    }
+    if (st < down + up) {
+      ptx::tc_fence_before();
+      __syncthreads();  // the stage before is free: drained, and its y read
+      issue(st + kWideStages - 1);
     }
   }
   copy_wait<0>();
+  if (given_up) {  // MMAs may be in flight still: they must not outlive their memory
+    if (tid == 0 && status) *status = MOE_ERR_TIMEOUT;
+    for (int st = max(0, down + up - kWideStages); st < down + up; ++st)
+      ptx::mbar_drain(&done[st & (kWideStages - 1)], (st >> 2) & 1, kWideWait);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kWideTmem);
+  }
   cluster_wait();
 }
 
 // ---------------------------------------------------------------- host
 namespace {
 
-template <typename T, typename Kern>
-cudaError_t adapters_with(Kern kern, int TM, int kstep, int smem, const AdapterArgs& a, cudaStream_t stream) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  const bool rest = a.out.p != a.y.p;  // rows without an adapter still have to be copied
-  const int tiles = (a.T < a.n ? a.T : a.n) + a.T / TM;  // at most this many
-  // as many blocks a tile as the machine holds at once and still have a step of k each
-  int cluster = 1;
-  while (cluster < kAdMaxCluster && 2 * tiles * cluster <= 3 * 148 && a.K > cluster * kstep) cluster *= 2;
-  const int kslice = ((a.K + cluster - 1) / cluster + 31) / 32 * 32;
-  const int nslice = ((a.N + cluster - 1) / cluster + 31) / 32 * 32;
-  return launch_cluster(kern, dim3((unsigned)tiles * cluster), dim3(kAdThreads), cluster, smem, stream,
-                        (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N, a.r, a.n, (const T*)a.A,
-                        (const T*)a.B, a.scale, a.perm, a.offsets, rest, cluster, kslice, nslice, (T*)a.out.p,
-                        a.out.ld);
+struct Shares {
+  int tiles, cluster, kslice, nslice;
+};
+// tiles: an upper bound on the tiles of TM rows.  A tile gets as many blocks as the machine
+// holds at once, each with at least a step of k; more where a block would read over `much`
+// bytes of its adapter (16-token tiles: one wave of small blocks is as fast as their latency,
+// but 1 MB of an adapter over 4 blocks took 16.4 us where 8 took 12.5).
+Shares shares_of(const AdapterArgs& a, int TM, int kstep, int64_t much) {
+  Shares s{(a.T < a.n ? a.T : a.n) + a.T / TM, 1, 0, 0};
+  auto more = [&] {
+    return 2 * s.tiles * s.cluster <= 3 * 148 || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
+  };
+  while (s.cluster < kAdMaxCluster && a.K > s.cluster * kstep && more()) s.cluster *= 2;
+  s.kslice = ((a.K + s.cluster - 1) / s.cluster + 31) / 32 * 32;
+  s.nslice = ((a.N + s.cluster - 1) / s.cluster + 31) / 32 * 32;
+  return s;
+}
+
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, int smem) {
+  return smem > 48 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
 }
 
 template <typename T, int NR>
 cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
   constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4)) * (int)sizeof(float);
-  return adapters_with<T>(adapter_kernel<T, NR>, 16, kAdWarps * 32, smem, a, s);
+  const Shares p = shares_of(a, 16, kAdWarps * 32, 96 * 1024);
+  const cudaError_t e = allow_smem(adapter_kernel<T, NR>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(adapter_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kAdThreads), p.cluster, smem, s,
+                        (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N, a.r, a.n, (const T*)a.A,
+                        (const T*)a.B, a.scale, a.perm, a.offsets, a.out.p != a.y.p, p.cluster, p.kslice, p.nslice,
+                        (T*)a.out.p, a.out.ld);
 }
 template <typename T, int NR>
 cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
-  return adapters_with<T>(adapter_wide_kernel<T, NR>, kWideTokens, 64, wide_smem_bytes<NR>(), a, s);
+  const Shares p = shares_of(a, kWideTokens, 64, INT64_MAX);
+  const cudaError_t e = allow_smem(adapter_wide_kernel<T, NR>, wide_smem_bytes<NR>());
+  if (e != cudaSuccess) return e;
+  return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kAdThreads), p.cluster,
+                        (size_t)wide_smem_bytes<NR>(), s, (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N,
+                        a.r, a.n, (const T*)a.A, (const T*)a.B, a.scale, a.perm, a.offsets, a.out.p != a.y.p, p.cluster,
+                        p.kslice, p.nslice, (T*)a.out.p, a.out.ld, a.status);
 }
 
 // Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of

@@ -157,7 +157,7 @@ extern "C" moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t 
 extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
                                    int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
                                    const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
-                                   int64_t ldo, cudaStream_t stream) {
+                                   int64_t ldo, int32_t* status, cudaStream_t stream) {
   if (!entries_ok(T, 1) || n < 1 || n > kMaxGroups || r < 8 || r > 128 || r % 8 != 0) return MOE_ERR_SHAPE;
   if (!width_ok(K) || !width_ok(N) || K % 8 != 0 || N % 8 != 0) return MOE_ERR_SHAPE;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_FORMAT;
@@ -166,7 +166,7 @@ extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, in
   if (!x || !y || !A || !B || !scale || !perm || !offsets || !out) return MOE_ERR_ARG;
   if (out == y && ldo != ldy) return MOE_ERR_ARG;
   if (!on(x, 16) || !on(y, 16) || !on(A, 16) || !on(B, 16) || !on(out, 16) || ldx % 8 != 0 || ldy % 8 != 0 ||
-      ldo % 8 != 0 || !on(scale, 4) || !on(perm, 4) || !on(offsets, 4))
+      ldo % 8 != 0 || !on(scale, 4) || !on(perm, 4) || !on(offsets, 4) || !on(status, 4))
     return MOE_ERR_ALIGN;
   const moe_status ds = check_device();
   if (ds != MOE_OK) return ds;
@@ -176,5 +176,6 @@ extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, in
   a.out = {out, ldo};
   a.T = T, a.K = K, a.N = N, a.r = r, a.n = n;
   a.A = A, a.B = B, a.scale = scale, a.perm = perm, a.offsets = offsets;
+  a.status = status;
   return launched(launch_adapters(a, dtype, stream));
 }

@@ -204,6 +204,7 @@ struct AdapterArgs {
   const void *A, *B;
   const float* scale;
   const int32_t *perm, *offsets;
+  int32_t* status;  // null, or where MOE_ERR_TIMEOUT goes
 };
 cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t stream);
 

@@ -227,15 +227,16 @@ def moe_swiglu_backward(dh: torch.Tensor, ckpt: SwigluCkpt, dg: torch.Tensor | N
 
 # ------------------------------------------------------------------ adapters
 def moe_adapters(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
-                 routes: Routes, out: torch.Tensor | None = None,
+                 routes: Routes, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """out = y + scale[a] * B[a] (A[a] x) for each token's adapter a (none: out = y).
 
     x [T, K], y and out [T, N] (out may be y), A [n, r, K] and B [n, N, r] contiguous, all
     bfloat16 or all float16; scale float32 [n]; routes = moe_sort(adapter of each token, n),
-    -1 for none."""
+    -1 for none.  status: int32 [1], zeroed by the caller, gets MOE_ERR_TIMEOUT if a bounded
+    wait of the kernel gave up (out is undefined then)."""
     return _moe_ops.adapters(x, y, A, B, scale, routes.perm, routes.inv, routes.offsets, routes.T, routes.k, routes.E,
-                             out, stream)
+                             out, status, stream)
 
 
 __all__ = ["ActCkpt", "Routes", "SwigluCkpt", "alloc_ckpt", "alloc_routes", "moe_act_load", "moe_act_save",

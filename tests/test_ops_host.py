@@ -30,7 +30,7 @@ ARGS = {
     "moe_swiglu_backward": dict(dh=FAKE, lddh=64, dtype=0, gq=FAKE, ge=FAKE, uq=FAKE, ue=FAKE, R=16, F=64, dg=FAKE,
                                 lddg=64, du=FAKE, lddu=64, h=FAKE, ldh=64, n_rows=None),
     "moe_adapters": dict(x=FAKE, ldx=64, y=FAKE, ldy=64, dtype=0, T=16, K=64, N=64, r=16, n=4, A=FAKE, B=FAKE, scale=FAKE,
-                         perm=FAKE, offsets=FAKE, out=FAKE + 65536, ldo=64),
+                         perm=FAKE, offsets=FAKE, out=FAKE + 65536, ldo=64, status=None),
 }
 
 
@@ -101,6 +101,7 @@ def test_alignment(name):
     if "ws" in a:
         assert call(name, ws=FAKE + 128) == "MOE_ERR_ALIGN"
     if name == "moe_adapters":
+        assert call(name, status=FAKE + 2) == "MOE_ERR_ALIGN"
         for key in ("x", "y", "A", "B", "out"):
             assert call(name, **{key: FAKE + 8}) == "MOE_ERR_ALIGN", key
         for key in ("ldx", "ldy", "ldo"):
