@@ -474,41 +474,55 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   const int chunk = tid & 7, row8 = tid >> 3;  // what the thread copies: 16-byte chunk of rows row8, row8 + 32
   const int src[2] = {token(row8), token(row8 + 32)};
   const int tok[2] = {token(16 * m + g), token(16 * m + 8 + g)};
-  const T* Aa = A + (int64_t)tile.adapter * r * K;
-  const T* Ba = B + (int64_t)tile.adapter * N * r;
   const int down = k1 > k0 ? (k1 - k0 + 63) / 64 : 0, up = n1 > n0 ? (n1 - n0 + 63) / 64 : 0;
-  auto swizzled = [](uint32_t tile_at, int row, int c) { return tile_at + row * 128 + ((c ^ (row & 7)) << 4); };
+  auto swizzled = [](int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); };
   auto stage_at = [&](int st) { return ring + (st & (kWideStages - 1)) * STAGE; };
+  // Stages are issued in order: what a thread copies next is kept in pointers that advance.
+  // Of x, A and y it copies one chunk of rows row8 + 32 i, 32 rows being 4096 bytes of a tile.
+  const uint32_t at_row = swizzled(row8, chunk);
+  int k_next = k0 + chunk * 8, n_next = n0 + chunk * 8;
+  const T* x_next[2] = {x + (int64_t)max(src[0], 0) * ldx + k_next, x + (int64_t)max(src[1], 0) * ldx + k_next};
+  const T* y_next[2] = {y + (int64_t)max(src[0], 0) * ldy + n_next, y + (int64_t)max(src[1], 0) * ldy + n_next};
+  const T* a_next = A + ((int64_t)tile.adapter * r + row8) * K + k_next;
+  const int64_t a_rows = (int64_t)32 * K;
+  // of B chunk b_chunk of outputs b_out + b_step i, which lie in permuted rows
+  constexpr int b_step = kAdThreads / NR;
+  const int b_chunk = tid % NR, b_out = tid / NR;
+  int b_left = n1 - n0 - b_out;
+  const T* b_next = B + ((int64_t)tile.adapter * N + n0 + b_out) * r + b_chunk * 8;
+  uint32_t at_b[NR / 4];
+#pragma unroll
+  for (int j = 0; j < NR / 4; ++j) {
+    const int o = b_out + b_step * j;
+    at_b[j] = kWideTile + (b_chunk >> 3) * kWideTile +
+              swizzled((o & 32) + ((o >> 1) & 3) * 8 + ((o >> 3) & 3) * 2 + (o & 1), b_chunk & 7);
+  }
   auto issue = [&](int st) {
-    const uint32_t base = stage_at(st), second = base + kWideTile;
+    const uint32_t base = stage_at(st);
     if (st < down) {
-      const int k = k0 + st * 64 + chunk * 8;
-      const bool in = k < k1;
+      const bool in = k_next < k1;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool real = in && src[h] >= 0;
-        copy16(swizzled(base, row8 + 32 * h, chunk), real ? x + (int64_t)src[h] * ldx + k : x, real);
+        copy16(base + at_row + 4096 * h, x_next[h], in && src[h] >= 0);
+        x_next[h] += 64;
       }
 #pragma unroll
-      for (int j = 0; j < NR / 4; ++j) {
-        const int row = row8 + 32 * j;
-        const bool real = in && row < r;
-        copy16(swizzled(second, row, chunk), real ? Aa + (int64_t)row * K + k : Aa, real);
-      }
+      for (int j = 0; j < NR / 4; ++j)
+        copy16(base + kWideTile + at_row + 4096 * j, a_next + a_rows * j, in && row8 + 32 * j < r);
+      a_next += 64;
+      k_next += 64;
     } else if (st < down + up) {
-      const int c0 = n0 + (st - down) * 64, c = c0 + chunk * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool real = c < n1 && src[h] >= 0;
-        copy16(swizzled(base, row8 + 32 * h, chunk), real ? y + (int64_t)src[h] * ldy + c : y, real);
+        copy16(base + at_row + 4096 * h, y_next[h], n_next < n1 && src[h] >= 0);
+        y_next[h] += 64;
       }
 #pragma unroll
-      for (int j = 0; j < NR / 4; ++j) {  // NR chunks a row
-        const int i = tid + kAdThreads * j, o = i / NR, b = i % NR;
-        const bool real = c0 + o < n1 && b * 8 < r;
-        const int row = (o & 32) + ((o >> 1) & 3) * 8 + ((o >> 3) & 3) * 2 + (o & 1);
-        copy16(swizzled(second + (b >> 3) * kWideTile, row, b & 7), real ? Ba + (int64_t)(c0 + o) * r + b * 8 : Ba, real);
-      }
+      for (int j = 0; j < NR / 4; ++j)
+        copy16(base + at_b[j], b_next + (int64_t)b_step * j * r, b_step * j < b_left && b_chunk * 8 < r);
+      b_next += (int64_t)64 * r;
+      b_left -= 64;
+      n_next += 64;
     }
     copy_commit();
   };
@@ -592,11 +606,16 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     uint32_t hi[2], lo[2];
     split2<T>(s.x, s.y, hi[0], lo[0]);
     split2<T>(s.z, s.w, hi[1], lo[1]);
-    const uint32_t at = swizzled((piece >> 4) * kWideTile, row, (piece & 15) >> 1) + (piece & 1) * 8;
+    const uint32_t at = (piece >> 4) * kWideTile + swizzled(row, (piece & 15) >> 1) + (piece & 1) * 8;
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_hi + at), "r"(hi[0]), "r"(hi[1]) : "memory");
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_lo + at), "r"(lo[0]), "r"(lo[1]) : "memory");
   }
   cluster_arrive();  // this warp has read; no block may leave before all have
+  // the lane's outputs of a stage: eight in a row of two tokens
+  const uint32_t at_y = swizzled(16 * m + g, 4 * half + q);  // eight rows further: 1024 bytes
+  int col = n0 + 32 * half + 8 * q;
+  T* o_next[2] = {out + (int64_t)max(tok[0], 0) * ldo + col, out + (int64_t)max(tok[1], 0) * ldo + col};
+  float back[2] = {1.0f, 1.0f};
   for (int st = down; st < down + up + 1; ++st) {
     if (st < down + up) {
       copy_wait<kWideStages - 2>();
@@ -619,19 +638,21 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
       }
     }
     if (st > down) {  // y + what the stage before came to
-      const int was = st - 1, col = n0 + (was - down) * 64 + 32 * half + 8 * q;
+      const int was = st - 1;
       wait_done(was);
       ptx::tc_fence_after();
       float acc[4][4];
       tmem_rows16<4>(tmem + my_lanes + 128 + (was & 1) * 64 + 32 * half, acc);
+      const uint32_t ys = stage_at(was) + at_y;
+      const uint4 yv[2] = {ptx::lds_v4(ys), ptx::lds_v4(ys + 1024)};
+      if (is_f16<T> && was == down) back[0] = undo[16 * m + g], back[1] = undo[16 * m + 8 + g];
       ptx::tmem_ld_wait();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (tok[h] < 0 || col >= n1) continue;
-        const int row = 16 * m + 8 * h + g;
-        store_sum<T>(out + (int64_t)tok[h] * ldo + col, ptx::lds_v4(swizzled(stage_at(was), row, 4 * half + q)), acc, h,
-                     is_f16<T> ? undo[row] : 1.0f);
+        if (tok[h] >= 0 && col < n1) store_sum<T>(o_next[h], yv[h], acc, h, back[h]);
+        o_next[h] += 64;
       }
+      col += 64;
     }
     if (st < down + up) {
       ptx::tc_fence_before();
