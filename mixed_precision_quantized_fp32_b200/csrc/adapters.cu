@@ -82,11 +82,11 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
     const int u = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += u;
   }
-  if (lane == 31) wsum[warp] = s;
+  if (lane == 31 && warp < kAdWarps) wsum[warp] = s;
   if (first) first[tid] = mine_of_perm;
   __syncthreads();
   int before = s - mine;
-  for (int w = 0; w < warp; ++w) before += wsum[w];
+  for (int w = 0; w < min(warp, kAdWarps); ++w) before += wsum[w];
   if (want >= before && want < before + mine) {
     for (int i = 0; i < per; ++i) {
       const int a = tid * per + i;
@@ -412,8 +412,9 @@ __device__ __forceinline__ void tmem_rows16(uint32_t taddr, float (&r)[X][4]) {
 // cluster, on tcgen05 with accumulators in tensor memory: at ranks of 64 the mma.sync form
 // spent half its time feeding and running the tensor cores beside the loads.  Operands come
 // through one ring of 64-wide stages in shared memory over both products: x and A, then y and
-// B.  All threads copy (cp.async: tokens are gathered, so there is no box for a TMA load);
-// one warp issues each stage's MMAs, whose completion frees the stage.
+// B.  Eight warps copy (cp.async: tokens are gathered, so there is no box for a TMA load) and
+// drain; a ninth issues the MMAs.  One block barrier a stage says that the stage has landed
+// and that the stage two before it has been drained, which is the one copied into next but two.
 //   D1[64][RP]  = sum over k of x A^T        tensor memory columns 0 .. 127
 //   D2[64][64]  = P_lo B^T + P_hi B^T        two buffers, columns 128 .. 255; one is drained
 //                                            and added to y while the next is computed
@@ -422,15 +423,17 @@ __device__ __forceinline__ void tmem_rows16(uint32_t taddr, float (&r)[X][4]) {
 // 64, with i = j/8 % 4 and c = j % 8, so that a lane of the epilogue has eight outputs in a row.
 // Two blocks share an SM; each asks for 256 of its 512 tensor-memory columns and for more than
 // a third of its shared memory, so that a third block never waits for columns.
-constexpr int kWideStages = 4;
+constexpr int kWideStages = 5;
+constexpr int kWideAhead = 3;  // stages copied ahead
+constexpr int kWideThreads = kAdThreads + 32;
 constexpr int kWideTokens = 64;
 constexpr uint32_t kWideTmem = 256;
 constexpr int kWideTile = 64 * 128;  // 64 rows of 128 bytes
 
 template <int NR> constexpr int wide_stage_bytes() { return kWideTile + (NR <= 8 ? kWideTile : 2 * kWideTile); }
 template <int NR> constexpr int wide_smem_bytes() {
-  const int need = 1024 + kWideStages * wide_stage_bytes<NR>() + 2 * (NR <= 8 ? 1 : 2) * kWideTile +
-                   kWideTokens * NR * 8 * 4 + kWideTokens * 4;
+  const int need = 1024 + kWideStages * wide_stage_bytes<NR>() + 2 * (NR <= 8 ? 1 : 2) * kWideTile + kWideTokens * 4 +
+                   (NR <= 8 ? 0 : kWideTokens * NR * 8 * 4);
   return need < 80 * 1024 ? 80 * 1024 : need;
 }
 
@@ -440,7 +443,7 @@ template <typename T> __host__ __device__ constexpr uint32_t wide_idesc(int N) {
 }
 
 template <typename T, int NR>
-__global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
     adapter_wide_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r,
                         int n, const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
                         const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
@@ -454,29 +457,31 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   __shared__ int given_up;
   const uint32_t ring = (ptx::smem_u32(wide_sm) + 1023u) & ~1023u;  // swizzled tiles start at multiples of 1024
   const uint32_t p_hi = ring + kWideStages * STAGE, p_lo = p_hi + KBLK * kWideTile;
-  float* mine = reinterpret_cast<float*>(wide_sm + (p_lo + KBLK * kWideTile - ptx::smem_u32(wide_sm)));  // [TM][RP]
-  float* undo = mine + TM * RP;  // [TM] fp16: what takes a row's power of two back
+  auto at_smem = [&](uint32_t a) { return reinterpret_cast<float*>(wide_sm + (a - ptx::smem_u32(wide_sm))); };
+  float* undo = at_smem(p_lo + KBLK * kWideTile);  // [TM] fp16: what takes a row's power of two back
   const uint32_t rank = cluster_rank();
   const int rest0 = rest ? min(max(__ldg(offsets + n), 0), T_) : T_;
   const Tile tile = find_tile(blockIdx.x / cluster, TM, offsets, n, T_, perm, nullptr);
   if (tile.rows == 0) {  // all blocks of the cluster alike
-    if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
+    if (rest && threadIdx.x < kAdThreads) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
     return;
   }
   const float sc = __ldg(scale + tile.adapter);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int m = warp & 3, half = warp >> 2;  // a warp reads 16 tokens' lanes of tensor memory, half of the columns
+  const bool drains = warp < kAdWarps;
+  const int m = warp & 3, half = (warp >> 2) & 1;  // a warp reads 16 tokens' lanes of tensor memory, half of the columns
   const int k0 = rank * kslice, k1 = min(K, k0 + kslice), n0 = rank * nslice, n1 = min(N, n0 + nslice);
   auto token = [&](int row) {
     const int t = row < tile.rows ? __ldg(perm + tile.row0 + row) : -1;
     return (unsigned)t < (unsigned)T_ ? t : -1;
   };
-  const int chunk = tid & 7, row8 = tid >> 3;  // what the thread copies: 16-byte chunk of rows row8, row8 + 32
+  const int chunk = tid & 7, row8 = (tid >> 3) & 31;  // what the thread copies: 16-byte chunk of rows row8, row8 + 32
   const int src[2] = {token(row8), token(row8 + 32)};
   const int tok[2] = {token(16 * m + g), token(16 * m + 8 + g)};
-  const int down = k1 > k0 ? (k1 - k0 + 63) / 64 : 0, up = n1 > n0 ? (n1 - n0 + 63) / 64 : 0;
+  // the same number of k stages in every block (zeros behind K), so that their shares of P lie alike
+  const int down = (kslice + 63) / 64, up = n1 > n0 ? (n1 - n0 + 63) / 64 : 0;
   auto swizzled = [](int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); };
-  auto stage_at = [&](int st) { return ring + (st & (kWideStages - 1)) * STAGE; };
+  auto stage_at = [&](int st) { return ring + (uint32_t)(st % kWideStages) * STAGE; };
   // Stages are issued in order: what a thread copies next is kept in pointers that advance.
   // Of x, A and y it copies one chunk of rows row8 + 32 i, 32 rows being 4096 bytes of a tile.
   const uint32_t at_row = swizzled(row8, chunk);
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   const int64_t a_rows = (int64_t)32 * K;
   // of B chunk b_chunk of outputs b_out + b_step i, which lie in permuted rows
   constexpr int b_step = kAdThreads / NR;
-  const int b_chunk = tid % NR, b_out = tid / NR;
+  const int b_chunk = tid % NR, b_out = (tid % kAdThreads) / NR;
   int b_left = n1 - n0 - b_out;
   const T* b_next = B + ((int64_t)tile.adapter * N + n0 + b_out) * r + b_chunk * 8;
   uint32_t at_b[NR / 4];
@@ -527,46 +532,49 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
     copy_commit();
   };
   auto wait_done = [&](int st) {  // of the stage's MMAs; bounded
-    if (!ptx::mbar_wait(&done[st & (kWideStages - 1)], (st >> 2) & 1, &given_up, kWideWait)) given_up = 1;
+    if (!ptx::mbar_wait(&done[st % kWideStages], (st / kWideStages) & 1, &given_up, kWideWait)) given_up = 1;
   };
+  if (drains) {
 #pragma unroll
-  for (int st = 0; st < kWideStages - 1; ++st) issue(st);
-  if (warp == 0) {
+    for (int st = 0; st < kWideAhead; ++st) issue(st);
+  } else {
     ptx::tmem_alloc(&tmem_at, kWideTmem);
     ptx::tmem_relinquish();  // at once: the SM's other block waits for the permit
+    if (lane == 0) {
+      for (int i = 0; i < kWideStages; ++i) ptx::mbar_init(&done[i], 1);
+      ptx::fence_mbar_init();
+      given_up = 0;
+    }
   }
-  if (tid == 0) {
-    for (int i = 0; i < kWideStages; ++i) ptx::mbar_init(&done[i], 1);
-    ptx::fence_mbar_init();
-    given_up = 0;
-  }
-  if (rest) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
+  if (rest && drains) copy_rest(y, ldy, out, ldo, N, rest0, T_, perm);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_at, my_lanes = (uint32_t)(m * 32) << 16;
   for (int st = 0; st < down; ++st) {
-    copy_wait<kWideStages - 2>();
+    copy_wait<kWideAhead - 1>();
     ptx::fence_proxy_async_smem();
     __syncthreads();
-    if (warp == 0) {
+    if (drains) {
+      if (st > 1) wait_done(st - 2);
+      issue(st + kWideAhead);
+    } else {
       const uint64_t xd = ptx::sw128_desc(stage_at(st)), ad = ptx::sw128_desc(stage_at(st) + kWideTile);
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // 16 values, 32 bytes, at a time
         ptx::mma_f16_ss_warp(tmem, xd + 2 * k, ad + 2 * k, wide_idesc<T>(RP), st || k ? 1u : 0u);
-      ptx::mma_commit_warp(&done[st & (kWideStages - 1)]);
+      ptx::mma_commit_warp(&done[st % kWideStages]);
     }
-    if (st > 0) wait_done(st - 1);
-    issue(st + kWideStages - 1);
   }
-  {  // this block's share of P; a block without k values has zeros
-    float acc[HALF][4] = {};
-    if (down > 0) {
-      wait_done(down - 1);
-      ptx::tc_fence_after();
-      tmem_rows16<HALF>(tmem + my_lanes + half * (RP / 2), acc);
-      ptx::tmem_ld_wait();
-    }
+  // This block's share of P lies behind the ring's last filled stage: there, unless it is too
+  // small for it, nothing is copied before the cluster has met again.
+  float* mine = at_smem(NR <= 8 ? stage_at(down + kWideStages - 1) : p_lo + KBLK * kWideTile + TM * 4);  // [TM][RP]
+  wait_done(down - 1);
+  if (drains) {
+    float acc[HALF][4];
+    ptx::tc_fence_after();
+    tmem_rows16<HALF>(tmem + my_lanes + half * (RP / 2), acc);
+    ptx::tmem_ld_wait();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -578,50 +586,55 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
   cluster_wait();
   // P: the blocks' shares added in order, in 16-byte pieces, and split into hi and lo terms
   constexpr int PIECES = RP / 4;  // lanes of a row, a power of two up to 32
+  if (drains)
 #pragma unroll 2
-  for (int c = tid; c < TM * PIECES; c += kAdThreads) {
-    const int row = c / PIECES, piece = c % PIECES;
-    float4 s = make_float4(0, 0, 0, 0);
-    if (piece * 4 < r && row < tile.rows) {  // the rank is a multiple of 8
-      float4 v[kAdMaxCluster];
+    for (int c = tid; c < TM * PIECES; c += kAdThreads) {
+      const int row = c / PIECES, piece = c % PIECES;
+      float4 s = make_float4(0, 0, 0, 0);
+      if (piece * 4 < r && row < tile.rows) {  // the rank is a multiple of 8
+        float4 v[kAdMaxCluster];
 #pragma unroll
-      for (int k = 0; k < kAdMaxCluster; ++k)
-        if (k < cluster) v[k] = load_remote4(mine + c * 4, k);
+        for (int k = 0; k < kAdMaxCluster; ++k)
+          if (k < cluster) v[k] = load_remote4(mine + c * 4, k);
 #pragma unroll
-      for (int k = 0; k < kAdMaxCluster; ++k)
-        if (k < cluster) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
-      s.x *= sc, s.y *= sc, s.z *= sc, s.w *= sc;
+        for (int k = 0; k < kAdMaxCluster; ++k)
+          if (k < cluster) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+        s.x *= sc, s.y *= sc, s.z *= sc, s.w *= sc;
+      }
+      if constexpr (is_f16<T>) {  // the row's lanes agree on its power of two
+        uint32_t big = max(max(__float_as_uint(s.x) & 0x7FFFFFFFu, __float_as_uint(s.y) & 0x7FFFFFFFu),
+                           max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
+#pragma unroll
+        for (int o = PIECES / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+        const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
+        const bool scaled = big < 0x7F800000u && e > 0;
+        const float by = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
+        s.x *= by, s.y *= by, s.z *= by, s.w *= by;
+        if (piece == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+      }
+      uint32_t hi[2], lo[2];
+      split2<T>(s.x, s.y, hi[0], lo[0]);
+      split2<T>(s.z, s.w, hi[1], lo[1]);
+      const uint32_t at = (piece >> 4) * kWideTile + swizzled(row, (piece & 15) >> 1) + (piece & 1) * 8;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_hi + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_lo + at), "r"(lo[0]), "r"(lo[1]) : "memory");
     }
-    if constexpr (is_f16<T>) {  // the row's lanes agree on its power of two
-      uint32_t big = max(max(__float_as_uint(s.x) & 0x7FFFFFFFu, __float_as_uint(s.y) & 0x7FFFFFFFu),
-                         max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
-#pragma unroll
-      for (int o = PIECES / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-      const bool scaled = big < 0x7F800000u && e > 0;
-      const float by = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
-      s.x *= by, s.y *= by, s.z *= by, s.w *= by;
-      if (piece == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
-    }
-    uint32_t hi[2], lo[2];
-    split2<T>(s.x, s.y, hi[0], lo[0]);
-    split2<T>(s.z, s.w, hi[1], lo[1]);
-    const uint32_t at = (piece >> 4) * kWideTile + swizzled(row, (piece & 15) >> 1) + (piece & 1) * 8;
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_hi + at), "r"(hi[0]), "r"(hi[1]) : "memory");
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_lo + at), "r"(lo[0]), "r"(lo[1]) : "memory");
-  }
-  cluster_arrive();  // this warp has read; no block may leave before all have
+  cluster_arrive();  // this warp has read; no block may overwrite its share or leave before all have
   // the lane's outputs of a stage: eight in a row of two tokens
   const uint32_t at_y = swizzled(16 * m + g, 4 * half + q);  // eight rows further: 1024 bytes
   int col = n0 + 32 * half + 8 * q;
   T* o_next[2] = {out + (int64_t)max(tok[0], 0) * ldo + col, out + (int64_t)max(tok[1], 0) * ldo + col};
   float back[2] = {1.0f, 1.0f};
   for (int st = down; st < down + up + 1; ++st) {
+    if (st == down + 1) cluster_wait();
     if (st < down + up) {
-      copy_wait<kWideStages - 2>();
+      copy_wait<kWideAhead - 1>();
       ptx::fence_proxy_async_smem();  // the first time of P's terms too
+      ptx::tc_fence_before();
       __syncthreads();
-      if (warp == 0) {
+      if (drains) {
+        issue(st + kWideAhead);
+      } else {
         ptx::tc_fence_after();
         const uint32_t d2 = tmem + 128 + (st & 1) * 64;
         const uint64_t bd = ptx::sw128_desc(stage_at(st) + kWideTile);
@@ -634,10 +647,10 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
             ptx::mma_f16_ss_warp(d2, pd + at, bd + at, wide_idesc<T>(64), term || k ? 1u : 0u);
           }
         }
-        ptx::mma_commit_warp(&done[st & (kWideStages - 1)]);
+        ptx::mma_commit_warp(&done[st % kWideStages]);
       }
     }
-    if (st > down) {  // y + what the stage before came to
+    if (st > down && drains) {  // y + what the stage before came to
       const int was = st - 1;
       wait_done(was);
       ptx::tc_fence_after();
@@ -654,25 +667,20 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
       }
       col += 64;
     }
-    if (st < down + up) {
-      ptx::tc_fence_before();
-      __syncthreads();  // the stage before is free: drained, and its y read
-      issue(st + kWideStages - 1);
-    }
   }
+  if (up == 0) cluster_wait();
   copy_wait<0>();
   if (given_up) {  // MMAs may be in flight still: they must not outlive their memory
     if (tid == 0 && status) *status = MOE_ERR_TIMEOUT;
     for (int st = max(0, down + up - kWideStages); st < down + up; ++st)
-      ptx::mbar_drain(&done[st & (kWideStages - 1)], (st >> 2) & 1, kWideWait);
+      ptx::mbar_drain(&done[st % kWideStages], (st / kWideStages) & 1, kWideWait);
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (!drains) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kWideTmem);
   }
-  cluster_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -717,7 +725,7 @@ cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
   const Shares p = shares_of(a, kWideTokens, 64, INT64_MAX);
   const cudaError_t e = allow_smem(adapter_wide_kernel<T, NR>, wide_smem_bytes<NR>());
   if (e != cudaSuccess) return e;
-  return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kAdThreads), p.cluster,
+  return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kWideThreads), p.cluster,
                         (size_t)wide_smem_bytes<NR>(), s, (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N,
                         a.r, a.n, (const T*)a.A, (const T*)a.B, a.scale, a.perm, a.offsets, a.out.p != a.y.p, p.cluster,
                         p.kslice, p.nslice, (T*)a.out.p, a.out.ld, a.status);
