@@ -689,14 +689,16 @@ namespace {
 struct Shares {
   int tiles, cluster, kslice, nslice;
 };
-// tiles: an upper bound on the tiles of TM rows.  A tile gets as many blocks as the machine
-// holds at once, each with at least a step of k; more where a block would read over `much`
-// bytes of its adapter (16-token tiles: one wave of small blocks is as fast as their latency,
-// but 1 MB of an adapter over 4 blocks took 16.4 us where 8 took 12.5).
-Shares shares_of(const AdapterArgs& a, int TM, int kstep, int64_t much) {
+// tiles: an upper bound on the tiles of TM rows, of which often a fifth is there in fact.  A
+// tile gets blocks, each with at least a step of k, while they stay within one and a half
+// times what the machine holds at once (per_sm: blocks an SM holds); 64-token tiles of 8192
+// tokens, r 64: 31.2 us with 2 blocks a tile, 37.6 with 1; r 128, one block an SM: 42.8 and
+// with 2 49.7.  16-token tiles get more where a block would read over `much` bytes of its
+// adapter: 1 MB over 4 blocks took 16.4 us, over 8 12.5.
+Shares shares_of(const AdapterArgs& a, int TM, int kstep, int per_sm, int64_t much) {
   Shares s{(a.T < a.n ? a.T : a.n) + a.T / TM, 1, 0, 0};
   auto more = [&] {
-    return 2 * s.tiles * s.cluster <= 3 * 148 || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
+    return 4 * s.tiles * s.cluster <= 3 * 148 * per_sm || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
   };
   while (s.cluster < kAdMaxCluster && a.K > s.cluster * kstep && more()) s.cluster *= 2;
   s.kslice = ((a.K + s.cluster - 1) / s.cluster + 31) / 32 * 32;
@@ -712,7 +714,7 @@ cudaError_t allow_smem(Kern kern, int smem) {
 template <typename T, int NR>
 cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
   constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4)) * (int)sizeof(float);
-  const Shares p = shares_of(a, 16, kAdWarps * 32, 96 * 1024);
+  const Shares p = shares_of(a, 16, kAdWarps * 32, NR <= 8 ? 2 : 1, 96 * 1024);
   const cudaError_t e = allow_smem(adapter_kernel<T, NR>, smem);
   if (e != cudaSuccess) return e;
   return launch_cluster(adapter_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kAdThreads), p.cluster, smem, s,
@@ -722,7 +724,7 @@ cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
 }
 template <typename T, int NR>
 cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
-  const Shares p = shares_of(a, kWideTokens, 64, INT64_MAX);
+  const Shares p = shares_of(a, kWideTokens, 64, NR <= 8 ? 2 : 1, INT64_MAX);
   const cudaError_t e = allow_smem(adapter_wide_kernel<T, NR>, wide_smem_bytes<NR>());
   if (e != cudaSuccess) return e;
   return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kWideThreads), p.cluster,
