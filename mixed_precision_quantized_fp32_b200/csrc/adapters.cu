@@ -27,10 +27,6 @@ constexpr int kAdWarps = 8;
 constexpr int kAdThreads = 32 * kAdWarps;
 constexpr int kAdMaxCluster = 8;
 constexpr long long kWideWait = 2000000000ll;  // cycles a wait on the tensor cores may take, about a second
-#ifndef XSHORT
-#define XSHORT 128
-#define XPER 16
-#endif
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -734,10 +730,14 @@ cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
 }
 
 // Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of
-// many adapters); tiles of 64 where adapters have rows enough to fill them.
+// many adapters) and for short batches of low rank; tiles of 64 where adapters have rows
+// enough to fill them.  K = N = 4096, 16- against 64-token tiles: 128 tokens 5.6 / 11.4 us
+// (r 16), 8.7 / 14.4 (r 64); 1024 tokens of r 16 11.9 / 16.4; 256 of r 64 11.8 / 14.4; 512 of
+// r 128 (K = N = 2048) 26.3 / 16.0; 2048 of r 64 49.9 / 33.8; 512 tokens over 64 adapters
+// 10.5 / 22.5.
 template <typename T>
 cudaError_t adapters_of(const AdapterArgs& a, cudaStream_t s) {
-  if (a.T <= XSHORT || a.T < XPER * a.n) {
+  if (a.T <= 128 || a.T < 16 * a.n || a.T * a.r <= 16384) {
     if (a.r <= 16) return adapters_short<T, 2>(a, s);
     if (a.r <= 32) return adapters_short<T, 4>(a, s);
     return a.r <= 64 ? adapters_short<T, 8>(a, s) : adapters_short<T, 16>(a, s);

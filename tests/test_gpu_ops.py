@@ -422,7 +422,8 @@ def bank(n, r, K, N, dtype):
 @pytest.mark.parametrize("T,K,N,r,n", [
     (1, 8, 8, 8, 1), (1, 4096, 4096, 16, 32), (5, 264, 40, 8, 3), (17, 256, 1000, 24, 2), (64, 512, 256, 16, 48),
     (128, 136, 520, 64, 5), (129, 2048, 264, 32, 4), (300, 512, 512, 40, 1), (700, 320, 264, 64, 7), (400, 264, 288, 128, 3),
-    (1000, 128, 128, 8, 1024), (260, 1032, 2056, 16, 6)])
+    (1000, 128, 128, 8, 1024), (260, 1032, 2056, 16, 6), (2100, 64, 40, 8, 2), (1500, 1000, 1048, 16, 3),
+    (1030, 200, 72, 24, 5), (520, 2056, 328, 40, 2), (300, 72, 2000, 120, 6), (3000, 8, 8, 128, 9)])
 def test_adapters(T, K, N, r, n, dtype):
     ids = index(T, 1, n, "holes" if T > 1 else "all")[:, 0]
     x, y = rnd(T, K, dtype=dtype), rnd(T, N, dtype=dtype, seed=1)
@@ -430,17 +431,19 @@ def test_adapters(T, K, N, r, n, dtype):
     x[ids < 0] = float("nan")                    # rows without an adapter are not read
     routes = moe.moe_sort(ids, n)
     want, mag = ref_adapters(x, y, A, B, scale, ids)
-    out = moe.moe_adapters(x, y, A, B, scale, routes)
-    assert adapters_near(out, want, mag, K, r, dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = moe.moe_adapters(x, y, A, B, scale, routes, status=status)
+    assert adapters_near(out, want, mag, K, r, dtype) and int(status) == 0
     assert torch.equal(out[ids < 0], y[ids < 0])
     z = y.clone()
     assert moe.moe_adapters(x, z, A, B, scale, routes, out=z) is z
     assert torch.equal(z, out)                   # in place: the same bits
 
 
+@pytest.mark.parametrize("T,r", [(200, 16), (700, 64)])
 @pytest.mark.parametrize("kind", ["none", "one"])
-def test_adapters_all_or_none(kind):
-    T, K, N, r, n = 200, 256, 264, 16, 4
+def test_adapters_all_or_none(kind, T, r):
+    K, N, n = 256, 264, 4
     ids = index(T, 1, n, kind)[:, 0]
     x, y = rnd(T, K, dtype=BF16), rnd(T, N, dtype=BF16, seed=1)
     A, B, scale = bank(n, r, K, N, BF16)
@@ -451,8 +454,9 @@ def test_adapters_all_or_none(kind):
         assert torch.equal(out, y)
 
 
-def test_adapters_through_views():
-    T, K, N, r, n = 150, 264, 520, 32, 5
+@pytest.mark.parametrize("T,r", [(150, 32), (600, 64)])   # tiles of 16 and of 64 tokens
+def test_adapters_through_views(T, r):
+    K, N, n = 264, 520, 5
     ids = index(T, 1, n, "holes")[:, 0]
     x, y = rnd(T, K, dtype=F16), rnd(T, N, dtype=F16, seed=1)
     A, B, scale = bank(n, r, K, N, F16)
@@ -467,9 +471,10 @@ def test_adapters_through_views():
     assert bool((mem == 7.0).all())
 
 
-def test_adapters_beyond_half_range():
+@pytest.mark.parametrize("T", [40, 600])
+def test_adapters_beyond_half_range(T):
     # A x beyond 65504 in fp16 while the result is in range: it is held in 32 bits
-    T, K, N, r, n = 40, 512, 128, 16, 2
+    K, N, r, n = 512, 128, 64, 2
     ids = index(T, 1, n, "all")[:, 0]
     x = rnd(T, K, dtype=F16, sigma=300.0)
     A, B, scale = rnd(n, r, K, dtype=F16, sigma=60.0), rnd(n, N, r, dtype=F16, sigma=2e-4), torch.ones(n, device="cuda")
@@ -480,9 +485,10 @@ def test_adapters_beyond_half_range():
     assert adapters_near(moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, n)), want, mag, K, r, F16)
 
 
-def test_adapters_keep_requests_apart():
+@pytest.mark.parametrize("T,r", [(33, 8), (900, 40)])
+def test_adapters_keep_requests_apart(T, r):
     # one request's NaN and another's infinity stay in their rows
-    T, K, N, r, n = 33, 256, 264, 8, 3
+    K, N, n = 256, 264, 3
     ids = index(T, 1, n, "all")[:, 0]
     x, y = rnd(T, K, dtype=BF16), rnd(T, N, dtype=BF16, seed=1)
     A, B, scale = bank(n, r, K, N, BF16)
@@ -502,12 +508,15 @@ def test_two_runs_give_the_same_bits():
     o, w, dy = rnd(T * k, H, dtype=BF16), rnd(T, k), rnd(T, H, dtype=BF16, seed=1)
     ids = index(T, 1, 30, "holes")[:, 0]
     A, B, scale = bank(30, 16, H, H, BF16)
+    wide = bank(3, 64, H, H, BF16)
+    wids = index(T, 1, 3, "holes")[:, 0]
 
     def go():
         r = moe.moe_sort(idx, E)
         do = torch.zeros(T * k, H, dtype=BF16, device="cuda")
         return [r.perm, r.inv, r.offsets, moe.moe_collect(o, w, r), *moe.moe_collect_backward(dy, o, w, r, do=do),
-                moe.moe_adapters(dy, o[:T], A, B, scale, moe.moe_sort(ids, 30))]
+                moe.moe_adapters(dy, o[:T], A, B, scale, moe.moe_sort(ids, 30)),
+                moe.moe_adapters(dy, o[:T], *wide, moe.moe_sort(wids, 3))]
 
     first = go()
     for _ in range(3):
@@ -521,13 +530,15 @@ def test_side_stream_and_graph_replay():
     x, idx, w = rnd(T, H, dtype=BF16), index(T, k, E, "holes"), rnd(T, k)
     ids = index(T, 1, 9, "holes")[:, 0]
     A, B, scale = bank(9, 16, H, H, BF16)
+    wide = bank(9, 64, H, H, BF16)
 
     def step(stream=None):
         xs, r = moe.moe_dispatch(x, idx, E, xs=torch.zeros(T * k, H, dtype=BF16, device="cuda"), stream=stream)
         y = moe.moe_collect(xs, w, r, stream=stream)
         h, kept = moe.moe_swiglu_save(xs, xs, rows=r.offsets[E:], stream=stream)
         y2 = moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, 9, stream=stream), stream=stream)
-        return y, y2, xs, r.perm
+        y3 = moe.moe_adapters(x, y, *wide, moe.moe_sort(ids, 9, stream=stream), stream=stream)
+        return y, y2, y3, xs, r.perm
 
     want = [t.clone() for t in step()]
     torch.cuda.synchronize()
