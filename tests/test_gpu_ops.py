@@ -501,6 +501,122 @@ def test_adapters_keep_requests_apart(T, r):
     assert bool(torch.isnan(out[7]).all()) and not bool(torch.isfinite(out[20]).any())
 
 
+# ------------------------------------------------------------------ offsets beyond 32 bits
+def test_rows_beyond_32_bit_offsets():
+    # 2.2e9 values: the last tokens' rows lie beyond 2^31 values (and 2^32 bytes) of the matrix
+    T, k, H = 33600, 8, 8192
+    idx = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    idx[:, 0] = 0
+    idx[T - 3:] = torch.arange(k, device="cuda").int()
+    r = moe.moe_sort(idx, k)
+    perm, inv, total = check_routes(r, idx, k)
+    o = torch.zeros(T * k, H, dtype=F16, device="cuda")
+    r.perm.copy_(torch.arange(T * k - 1, -1, -1, device="cuda"))      # rows of o from its end
+    far = torch.where(r.inv >= 0, T * k - 1 - r.inv, -1).int()
+    routes = moe.Routes(T, k, k, r.perm, far, r.offsets)
+    v = rnd(T, H, dtype=F16)
+    rows = far.reshape(T, k)[:, 0].long()
+    o[rows] = v
+    o[far.reshape(T, k)[T - 3:].long().reshape(-1)] = v[T - 3:].repeat_interleave(k, 0)
+    w = torch.zeros(T, k, device="cuda")
+    w[:, 0] = 0.5
+    w[T - 3:, k - 1] = 0.25
+    y = moe.moe_collect(o, w, routes)
+    assert torch.equal(y[:T - 3], v[:T - 3] * 0.5) and torch.equal(y[T - 3:], v[T - 3:] * 0.75)
+    do, dw = moe.moe_collect_backward(v, o, w, routes, do=o.zero_())
+    assert torch.equal(do[rows], v * 0.5) and torch.equal(do[far.reshape(T, k)[T - 1, k - 1].long()], v[T - 1] * 0.25)
+    xs, r2 = moe.moe_dispatch(v, idx, k, xs=do)
+    assert torch.equal(xs[r2.inv.reshape(T, k)[:, 0].long()], v)
+
+
+def test_checkpoints_beyond_32_bit_offsets():
+    R, F = 70000, 32768                                   # 2.3e9 values
+    x = torch.zeros(R, F, dtype=BF16, device="cuda")
+    x[-3:] = rnd(3, F, dtype=BF16)
+    c = moe.moe_act_save(x)
+    codes, exps, vals = ref_ckpt(x[-3:])
+    np.testing.assert_array_equal(c.codes[-3:].cpu().numpy(), codes)
+    np.testing.assert_array_equal(c.exps[-3:].cpu().numpy(), exps)
+    del x
+    back = moe.moe_act_load(c)
+    np.testing.assert_array_equal(back[-3:].cpu().to(F64).numpy(), vals)
+    assert not bool(back[:4].any())
+    v = moe.ActCkpt(c.codes[-3:], c.exps[-3:], BF16)      # a slice of rows is a checkpoint too
+    np.testing.assert_array_equal(moe.moe_act_load(v).cpu().to(F64).numpy(), vals)
+
+
+# ------------------------------------------------------------------ refusals of the binding
+def test_binding_refuses_what_does_not_fit():
+    T, k, E, H = 6, 2, 3, 32
+    x, idx, w = rnd(T, H, dtype=BF16), index(T, k, E, "all"), rnd(T, k)
+    xs, r = moe.moe_dispatch(x, idx, E)
+    c, sc = moe.moe_act_save(x), moe.moe_swiglu_save(x, x)[1]
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    A, B, scale = bank(2, 8, H, H, BF16)
+    ar = moe.moe_sort(ids, 2)
+    bad = {
+        "types": lambda: moe.moe_dispatch(x.double(), idx, E), "idx type": lambda: moe.moe_sort(idx.long(), E),
+        "idx strides": lambda: moe.moe_sort(torch.stack([idx, idx], 2)[:, :, 0], E), "cpu idx": lambda: moe.moe_dispatch(x, idx.cpu(), E),
+        "x rank": lambda: moe.moe_dispatch(x[0], idx, E), "tokens": lambda: moe.moe_dispatch(x[:5], idx, E),
+        "xs shape": lambda: moe.moe_dispatch(x, idx, E, xs=xs[:5]), "xs type": lambda: moe.moe_dispatch(x, idx, E, xs=xs.half()),
+        "routes": lambda: moe.moe_dispatch(x, idx, E + 1, routes=r), "columns": lambda: moe.moe_collect(xs.t().contiguous().t(), w, r),
+        "w type": lambda: moe.moe_collect(xs, w.half(), r), "w shape": lambda: moe.moe_collect(xs, w[:, :1], r),
+        "y": lambda: moe.moe_collect(xs, w, r, y=x[:, :16]), "dy": lambda: moe.moe_collect_backward(xs, xs, w, r),
+        "not a tensor": lambda: moe.moe_collect(xs, 1.0, r), "E": lambda: moe.moe_sort(idx, 2 ** 40),
+        "ckpt type": lambda: moe.moe_act_save(x.half(), ckpt=c), "ckpt shape": lambda: moe.moe_act_save(x[:3], ckpt=c),
+        "load shape": lambda: moe.moe_act_load(c, x=x[:3]), "swiglu": lambda: moe.moe_swiglu_save(x, x[:3]),
+        "swiglu ckpt": lambda: moe.moe_swiglu_backward(x[:3], sc), "swiglu type": lambda: moe.moe_swiglu_save(x.float(), x.float(), ckpt=sc),
+        "rows": lambda: moe.moe_act_save(x, rows=ids), "A": lambda: moe.moe_adapters(x, x, A[:, :, :16], B, scale, ar),
+        "B": lambda: moe.moe_adapters(x, x, A, B[:1], scale, ar), "scale": lambda: moe.moe_adapters(x, x, A, B, scale[:1], ar),
+        "adapter routes": lambda: moe.moe_adapters(x, x, A, B, scale, r), "adapters' ws": lambda: moe.moe_sort(idx, E, ws=ids.cpu()),
+    }
+    for name, call in bad.items():
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(name)
+    refused = {
+        "E": (lambda: moe.moe_sort(idx, 1025), "MOE_ERR_SHAPE"), "k": (lambda: moe.moe_sort(torch.zeros(2, 9, dtype=torch.int32, device="cuda"), 3), "MOE_ERR_SHAPE"),
+        "pitch 0": (lambda: moe.moe_act_save(x[:1].expand(4, H)), "MOE_ERR_SHAPE"),
+        "fp32 adapters": (lambda: moe.moe_adapters(x.float(), x.float(), A.float(), B.float(), scale, ar), "MOE_ERR_FORMAT"),
+        "rank": (lambda: moe.moe_adapters(x, x, A[:, :4].contiguous(), B[:, :, :4].contiguous(), scale, ar), "MOE_ERR_SHAPE"),
+        "alignment": (lambda: moe.moe_adapters(spaced(x, 64, 4)[0], x, A, B, scale, ar), "MOE_ERR_ALIGN"),
+        "pitch": (lambda: moe.moe_adapters(spaced(x, 36)[0], x, A, B, scale, ar), "MOE_ERR_ALIGN"),
+    }
+    for name, (call, status) in refused.items():
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.name == status, name
+    torch.cuda.synchronize()
+
+
+def test_two_calls_at_once():
+    # two streams, two host threads: calls share nothing
+    import threading
+    T, k, E, H = 3000, 8, 64, 512                          # 24000 entries: the sort that needs a workspace
+    A, B, scale = bank(4, 64, H, H, BF16)
+    jobs = [(rnd(T, H, dtype=BF16, seed=i), index(T, k, E, "holes", seed=i), index(T, 1, 4, "holes", seed=i)[:, 0]) for i in (1, 2)]
+
+    def work(x, idx, ids, stream=None):
+        xs, r = moe.moe_dispatch(x, idx, E, xs=None, stream=stream)
+        return r.perm, moe.moe_dispatch_backward(xs, r, stream=stream), moe.moe_adapters(x, x, A, B, scale, moe.moe_sort(ids, 4, stream=stream), stream=stream)
+
+    want = [work(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got, streams = [None, None], [torch.cuda.Stream() for _ in jobs]
+
+    def run(i):
+        for _ in range(20):
+            got[i] = work(*jobs[i], stream=streams[i])
+        streams[i].synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ calls as programs make them
 def test_two_runs_give_the_same_bits():
     T, k, E, H = 2500, 4, 64, 512
