@@ -93,7 +93,8 @@ def test_sort(T, k, E, kind):
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("T,k,E,H,kind", [
     (0, 2, 8, 64, "all"), (1, 1, 4, 1, "all"), (16, 6, 256, 2048, "all"), (37, 3, 5, 77, "holes"),
-    (200, 8, 64, 12, "outside"), (1500, 2, 8, 130, "padded"), (300, 4, 16, 1001, "holes"), (400, 3, 9, 264, "none")])
+    (200, 8, 64, 12, "outside"), (16385, 1, 1024, 24, "outside"), (8192, 6, 256, 64, "all"), (65536, 1, 3, 8, "padded"),
+    (5471, 3, 300, 33, "holes"), (8191, 8, 256, 40, "none"), (2731, 7, 77, 520, "one"), (13108, 5, 6, 16, "holes"), (1500, 2, 8, 130, "padded"), (300, 4, 16, 1001, "holes"), (400, 3, 9, 264, "none")])
 def test_dispatch(T, k, E, H, kind, dtype):
     idx, x = index(T, k, E, kind), rnd(T, H, dtype=dtype)
     xs = torch.full((T * k, H), 5.0, dtype=dtype, device="cuda")
