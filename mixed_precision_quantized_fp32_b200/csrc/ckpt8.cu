@@ -18,7 +18,7 @@
 // Memory bounds all of these.  A quad of lanes takes one group, eight values a lane, so
 // bf16 loads are 16 bytes and code stores 8 bytes a lane, consecutive over the warp, and
 // the group's maximum takes two shuffles.  Rows whose pitch or start does not allow that
-// run one lane per value.
+// run with one value a lane and group.
 #include <initializer_list>
 
 #include "ops_common.cuh"
@@ -314,23 +314,67 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(
 }
 
 // ---------------------------------------------------------------- one value a lane
-__device__ __forceinline__ Place place1(uint32_t at, int G, int rows, int F) {
-  Place p;
-  p.row = at / (uint32_t)G;
-  p.grp = (int)(at - (uint32_t)p.row * (uint32_t)G);
-  p.col = p.grp * kGroup + (threadIdx.x & 31);
-  p.in = p.row < rows && p.col < F;
-  return p;
+// Any width, pitch and alignment: a warp takes S consecutive groups of a row, one value of
+// each a lane, so that loads and stores are consecutive over the warp and S of them are in
+// flight, and the row is found once for 32 S values.
+constexpr int kSpan = 8;       // groups a warp of save and load takes
+constexpr int kSpanSwiglu = 4; // of the SwiGLU kernels, which read two or three matrices
+
+// The warp's groups [grp, grp + S) of row `row`, its lane's first column and what is left of
+// the row from there.
+struct Span {
+  int64_t row;
+  int grp, col, left;
+  bool in;
+};
+template <int S>
+__device__ __forceinline__ Span span_of(int G, int rows, int F) {
+  const uint32_t spans = (uint32_t)(G + S - 1) / S, at = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const uint32_t row = at / spans;
+  Span s;
+  s.row = row;
+  s.grp = (int)(at - row * spans) * S;
+  s.col = s.grp * kGroup + (threadIdx.x & 31);
+  s.left = F - s.col;
+  s.in = row < (uint32_t)rows;
+  return s;
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t warp_exp(float v) {
-  return group_exp<T>(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+template <typename T, int S>
+__device__ __forceinline__ void load_span(const T* __restrict__ p, int left, float (&v)[S]) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) v[i] = i * kGroup < left ? to_f32<T>(__ldg(p + i * kGroup)) : 0.0f;
 }
-template <typename T>
-__device__ __forceinline__ int8_t encode1(float v, uint32_t eb) {
-  if (eb == 255u) return 0;
-  return (int8_t)(code_bits(clamp127(v * inv_step(eb)), 1.0f) & 0xFFu);
+template <typename T, int S>
+__device__ __forceinline__ void store_span(T* p, int left, const float (&v)[S]) {
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (i * kGroup < left) p[i * kGroup] = from_f32<T>(v[i]);
+}
+
+// Codes and exponents of the warp's groups; the first S lanes store one exponent each.
+template <typename T, int S>
+__device__ __forceinline__ void encode_span(const float (&v)[S], int left, int groups, int8_t* q, uint8_t* ex) {
+  const int lane = threadIdx.x & 31;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const uint32_t eb = group_exp<T>(__reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu));
+    if (lane == i) mine = eb;
+    if (i * kGroup < left)
+      q[i * kGroup] = eb == 255u ? (int8_t)0 : (int8_t)(code_bits(clamp127(v[i] * inv_step(eb)), 1.0f) & 0xFFu);
+  }
+  if (lane < S && lane < groups) ex[lane] = (uint8_t)mine;
+}
+template <int S>
+__device__ __forceinline__ void decode_span(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex, int left,
+                                            int groups, float (&v)[S]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = lane < S && lane < groups ? __ldg(ex + lane) : 0u;
+#pragma unroll
+  for (int i = 0; i < S; ++i) v[i] = i * kGroup < left ? (float)__ldg(q + i * kGroup) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < S; ++i) v[i] *= step_of(__shfl_sync(0xffffffffu, mine, i));
 }
 
 template <typename T>
@@ -338,13 +382,12 @@ __global__ void __launch_bounds__(256) act_save1_kernel(const T* __restrict__ x,
                                                         int8_t* __restrict__ q, uint8_t* __restrict__ ex,
                                                         const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place1(blockIdx.x * 8u + (threadIdx.x >> 5), G, rows, F);
-  const float v = p.in ? to_f32<T>(__ldg(x + p.row * ldx + p.col)) : 0.0f;
-  const uint32_t eb = warp_exp<T>(v);
-  if (!p.in) return;
-  q[p.row * F + p.col] = encode1<T>(v, eb);
-  if ((threadIdx.x & 31) == 0) ex[p.row * G + p.grp] = (uint8_t)eb;
+  const int G = (F + kGroup - 1) / kGroup;
+  const Span s = span_of<kSpan>(G, row_count(R, n_rows), F);
+  if (!s.in) return;
+  float v[kSpan];
+  load_span<T>(x + s.row * ldx + s.col, s.left, v);
+  encode_span<T>(v, s.left, G - s.grp, q + s.row * F + s.col, ex + s.row * G + s.grp);
 }
 
 template <typename T>
@@ -352,10 +395,12 @@ __global__ void __launch_bounds__(256) act_load1_kernel(const int8_t* __restrict
                                                         int R, int F, T* __restrict__ x, int64_t ldx,
                                                         const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place1(blockIdx.x * 8u + (threadIdx.x >> 5), G, rows, F);
-  if (!p.in) return;
-  x[p.row * ldx + p.col] = from_f32<T>((float)q[p.row * F + p.col] * step_of(__ldg(ex + p.row * G + p.grp)));
+  const int G = (F + kGroup - 1) / kGroup;
+  const Span s = span_of<kSpan>(G, row_count(R, n_rows), F);
+  if (!s.in) return;
+  float v[kSpan];
+  decode_span(q + s.row * F + s.col, ex + s.row * G + s.grp, s.left, G - s.grp, v);
+  store_span<T>(x + s.row * ldx + s.col, s.left, v);
 }
 
 template <typename T>
@@ -366,19 +411,18 @@ __global__ void __launch_bounds__(256) swiglu_save1_kernel(const T* __restrict__
                                                            uint8_t* __restrict__ ue,
                                                            const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place1(blockIdx.x * 8u + (threadIdx.x >> 5), G, rows, F);
-  const float a = p.in ? to_f32<T>(__ldg(g + p.row * ldg + p.col)) : 0.0f;
-  const float b = p.in ? to_f32<T>(__ldg(u + p.row * ldu + p.col)) : 0.0f;
-  const uint32_t ea = warp_exp<T>(a), eb = warp_exp<T>(b);
-  if (!p.in) return;
-  gq[p.row * F + p.col] = encode1<T>(a, ea);
-  uq[p.row * F + p.col] = encode1<T>(b, eb);
-  if ((threadIdx.x & 31) == 0) {
-    ge[p.row * G + p.grp] = (uint8_t)ea;
-    ue[p.row * G + p.grp] = (uint8_t)eb;
-  }
-  h[p.row * ldh + p.col] = from_f32<T>(swiglu(a, b));
+  const int G = (F + kGroup - 1) / kGroup;
+  const Span s = span_of<kSpanSwiglu>(G, row_count(R, n_rows), F);
+  if (!s.in) return;
+  float a[kSpanSwiglu], b[kSpanSwiglu];
+  load_span<T>(g + s.row * ldg + s.col, s.left, a);
+  load_span<T>(u + s.row * ldu + s.col, s.left, b);
+  const int64_t at = s.row * F + s.col, e_at = s.row * G + s.grp;
+  encode_span<T>(a, s.left, G - s.grp, gq + at, ge + e_at);
+  encode_span<T>(b, s.left, G - s.grp, uq + at, ue + e_at);
+#pragma unroll
+  for (int i = 0; i < kSpanSwiglu; ++i) a[i] = swiglu(a[i], b[i]);
+  store_span<T>(h + s.row * ldh + s.col, s.left, a);
 }
 
 template <typename T>
@@ -387,15 +431,22 @@ __global__ void __launch_bounds__(256) swiglu_backward1_kernel(
     const int8_t* __restrict__ uq, const uint8_t* __restrict__ ue, int R, int F, T* __restrict__ dg, int64_t lddg,
     T* __restrict__ du, int64_t lddu, T* __restrict__ h, int64_t ldh, const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int G = (F + kGroup - 1) / kGroup, rows = row_count(R, n_rows);
-  const Place p = place1(blockIdx.x * 8u + (threadIdx.x >> 5), G, rows, F);
-  if (!p.in) return;
-  const int64_t at = p.row * F + p.col, ge_at = p.row * G + p.grp;
-  const Grads r = swiglu_grad((float)gq[at] * step_of(__ldg(ge + ge_at)), (float)uq[at] * step_of(__ldg(ue + ge_at)),
-                              to_f32<T>(__ldg(dh + p.row * lddh + p.col)));
-  dg[p.row * lddg + p.col] = from_f32<T>(r.dg);
-  du[p.row * lddu + p.col] = from_f32<T>(r.du);
-  if (h) h[p.row * ldh + p.col] = from_f32<T>(r.h);
+  const int G = (F + kGroup - 1) / kGroup;
+  const Span s = span_of<kSpanSwiglu>(G, row_count(R, n_rows), F);
+  if (!s.in) return;
+  const int64_t at = s.row * F + s.col, e_at = s.row * G + s.grp;
+  float d[kSpanSwiglu], a[kSpanSwiglu], b[kSpanSwiglu];
+  load_span<T>(dh + s.row * lddh + s.col, s.left, d);
+  decode_span(gq + at, ge + e_at, s.left, G - s.grp, a);
+  decode_span(uq + at, ue + e_at, s.left, G - s.grp, b);
+#pragma unroll
+  for (int i = 0; i < kSpanSwiglu; ++i) {
+    const Grads r = swiglu_grad(a[i], b[i], d[i]);
+    d[i] = r.dg, a[i] = r.du, b[i] = r.h;
+  }
+  store_span<T>(dg + s.row * lddg + s.col, s.left, d);
+  store_span<T>(du + s.row * lddu + s.col, s.left, a);
+  if (h) store_span<T>(h + s.row * ldh + s.col, s.left, b);
 }
 
 // ---------------------------------------------------------------- host
@@ -420,9 +471,11 @@ Way way_of(int es, int F, std::initializer_list<Matrix> rows, std::initializer_l
   return !eight ? Way::kOne : flat ? Way::kFlat : Way::kEight;
 }
 
-dim3 grid_of(Way w, int R, int F) {
-  const uint64_t groups = (uint64_t)R * ((F + kGroup - 1) / kGroup), per = w == Way::kOne ? 8 : kGroupsPerBlock;
-  return dim3((unsigned)((groups + per - 1) / per));
+// span: groups a warp of the one-value kernel takes.
+dim3 grid_of(Way w, int R, int F, int span) {
+  const uint64_t G = (F + kGroup - 1) / kGroup;
+  if (w == Way::kOne) return dim3((unsigned)((R * ((G + span - 1) / span) + 7) / 8));
+  return dim3((unsigned)((R * G + kGroupsPerBlock - 1) / kGroupsPerBlock));
 }
 
 #define MOE_PICK(w, name, T) \
@@ -431,27 +484,27 @@ dim3 grid_of(Way w, int R, int F) {
 template <typename T>
 cudaError_t save_as(ConstRows x, int R, int F, Ckpt c, const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
-  return launch_chained(MOE_PICK(w, act_save, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)x.p, x.ld, R, F, c.q, c.e,
+  return launch_chained(MOE_PICK(w, act_save, T), grid_of(w, R, F, kSpan), dim3(256), 0, s, (const T*)x.p, x.ld, R, F, c.q, c.e,
                         n_rows);
 }
 template <typename T>
 cudaError_t load_as(Ckpt c, int R, int F, Rows x, const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
-  return launch_chained(MOE_PICK(w, act_load, T), grid_of(w, R, F), dim3(256), 0, s, (const int8_t*)c.q,
+  return launch_chained(MOE_PICK(w, act_load, T), grid_of(w, R, F, kSpan), dim3(256), 0, s, (const int8_t*)c.q,
                         (const uint8_t*)c.e, R, F, (T*)x.p, x.ld, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_save_as(ConstRows g, ConstRows u, int R, int F, Rows h, Ckpt cg, Ckpt cu, const int32_t* n_rows,
                            cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{g.p, g.ld}, {u.p, u.ld}, {h.p, h.ld}}, {cg.q, cu.q});
-  return launch_chained(MOE_PICK(w, swiglu_save, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)g.p, g.ld,
+  return launch_chained(MOE_PICK(w, swiglu_save, T), grid_of(w, R, F, kSpanSwiglu), dim3(256), 0, s, (const T*)g.p, g.ld,
                         (const T*)u.p, u.ld, R, F, (T*)h.p, h.ld, cg.q, cg.e, cu.q, cu.e, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_backward_as(ConstRows dh, Ckpt cg, Ckpt cu, int R, int F, Rows dg, Rows du, Rows h,
                                const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{dh.p, dh.ld}, {dg.p, dg.ld}, {du.p, du.ld}, {h.p, h.ld}}, {cg.q, cu.q});
-  return launch_chained(MOE_PICK(w, swiglu_backward, T), grid_of(w, R, F), dim3(256), 0, s, (const T*)dh.p, dh.ld,
+  return launch_chained(MOE_PICK(w, swiglu_backward, T), grid_of(w, R, F, kSpanSwiglu), dim3(256), 0, s, (const T*)dh.p, dh.ld,
                         (const int8_t*)cg.q, (const uint8_t*)cg.e, (const int8_t*)cu.q, (const uint8_t*)cu.e, R, F,
                         (T*)dg.p, dg.ld, (T*)du.p, du.ld, (T*)h.p, h.ld, n_rows);
 }
