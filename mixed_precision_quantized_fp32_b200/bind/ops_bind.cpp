@@ -219,16 +219,12 @@ void entries(const at::Tensor& idx, int32_t* T, int32_t* k) {
   *k = idx.dim() == 2 ? extent(idx.size(1), "k") : 1;
 }
 
-// New routes as one piece of memory: (perm, inv, offsets)
+// New routes: (perm, inv, offsets)
 PyObject* new_routes(const Call& c, int64_t R, int64_t E, Routes* r) {
   if (E < 0) refuse("E must not be negative, got ", E);
-  at::Tensor m = c.empty({2 * R + E + 1}, at::kInt);
-  int32_t* p = (int32_t*)m.data_ptr();
-  *r = {p, p + R, p + 2 * R};
-  PyObject* a = wrap(m.narrow(0, 0, R));
-  PyObject* b = wrap(m.narrow(0, R, R));
-  PyObject* o = wrap(m.narrow(0, 2 * R, E + 1));
-  return Py_BuildValue("(NNN)", a, b, o);
+  const at::Tensor perm = c.empty({R}, at::kInt), inv = c.empty({R}, at::kInt), offsets = c.empty({E + 1}, at::kInt);
+  *r = {(int32_t*)perm.data_ptr(), (int32_t*)inv.data_ptr(), (int32_t*)offsets.data_ptr()};
+  return Py_BuildValue("(NNN)", wrap(perm), wrap(inv), wrap(offsets));
 }
 
 // sort(idx, E, perm, inv, offsets, ws, stream): None, or (perm, inv, offsets) where perm is None

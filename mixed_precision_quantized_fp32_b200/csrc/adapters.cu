@@ -8,16 +8,24 @@
 //   P[row][r] = sum_k x[k] A_a[r][k]
 // in fp32, the blocks read one another's shares from distributed shared memory and add
 // them in order, and each block then has a share of the outputs for scale * P B_a^T + y.
-// One launch, no workspace, nothing added in global memory.
+// One launch, no workspace, nothing added in global memory.  (Down and up product as two
+// launches with partial sums in a workspace took 9.6 us for 64 requests where this takes
+// 6.6, and 104 us for the long batch below.)
 //
-// Arithmetic per byte is about the rank, far below what the tensor cores need to be the
-// bound, so operands go from memory straight to mma.sync fragments: the contraction
-// index may be permuted if both operands are permuted alike, and with a lane taking
-// eight consecutive values (16 bytes) of its row as its share of 32, every load is a
-// full 16 bytes and nothing is staged in shared memory.  The up product's fp32 operand P
-// goes in as two terms of the value type (P = hi + lo, 16 or more bits), so its rounding
-// stays far below that of the stored result; in fp16 a row is first brought to at most
-// 2^14 by a power of two, since P may pass fp16's range.
+// The up product's fp32 operand P goes in as two terms of the value type (P = hi + lo, 16 or
+// more bits), so its rounding stays far below that of the stored result; in fp16 a row is
+// first brought to at most 2^14 by a power of two, since P may pass fp16's range.
+//
+// Two kernels.  Decode batches: tiles of 16 tokens on mma.sync, operands from memory straight
+// to fragments (the contraction index may be permuted if both operands are permuted alike,
+// so a lane takes eight consecutive values, 16 bytes, of its row).  What bounds it is the
+// chain of latencies: finding the tile 0.8 us, loads and product 0.9, the cluster's meeting
+// 1.3, the second product 0.9.  K = N = 4096, r 16: 1 token 4.9 us, 64 requests of 48 adapters
+// 6.6 us; 64 requests of r 64 (69 MB of adapters) 12.2 us, 87% of the copy rate.
+// Long batches: tiles of 64 tokens on tcgen05 (adapter_wide_kernel).  8192 tokens, K = N =
+// 2048, r 64 (113 MB): 31 us, 56% of the copy rate; r 128 43 us.  Each block goes through
+// finding its tile, the down product, the cluster's meeting and the up product once, all blocks
+// at the same time, so memory idles in the meetings; mma.sync in its place took 38 and 76 us.
 #include "ops_common.cuh"
 #include "tc_ptx.cuh"
 
