@@ -26,6 +26,8 @@
 // 2048, r 64 (113 MB): 31 us, 56% of the copy rate; r 128 43 us.  Each block goes through
 // finding its tile, the down product, the cluster's meeting and the up product once, all blocks
 // at the same time, so memory idles in the meetings; mma.sync in its place took 38 and 76 us.
+#include <algorithm>
+
 #include "ops_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -694,7 +696,7 @@ struct Shares {
   int tiles, cluster, kslice, nslice;
 };
 // tiles: an upper bound on the tiles of TM rows, of which often a fifth is there in fact.  A
-// tile gets blocks, each with at least a step of k, while they stay within one and a half
+// tile gets blocks, each with at least a step of k or of outputs, while they stay within one and a half
 // times what the machine holds at once (per_sm: blocks an SM holds); 64-token tiles of 8192
 // tokens, r 64: 31.2 us with 2 blocks a tile, 37.6 with 1; r 128, one block an SM: 42.8 and
 // with 2 49.7.  16-token tiles get more where a block would read over `much` bytes of its
@@ -704,7 +706,7 @@ Shares shares_of(const AdapterArgs& a, int TM, int kstep, int per_sm, int64_t mu
   auto more = [&] {
     return 4 * s.tiles * s.cluster <= 3 * 148 * per_sm || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
   };
-  while (s.cluster < kAdMaxCluster && a.K > s.cluster * kstep && more()) s.cluster *= 2;
+  while (s.cluster < kAdMaxCluster && std::max(a.K, a.N) > s.cluster * kstep && more()) s.cluster *= 2;
   s.kslice = ((a.K + s.cluster - 1) / s.cluster + 31) / 32 * 32;
   s.nslice = ((a.N + s.cluster - 1) / s.cluster + 31) / 32 * 32;
   return s;

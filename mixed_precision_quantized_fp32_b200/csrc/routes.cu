@@ -351,9 +351,10 @@ __device__ __forceinline__ void entries_of(int64_t t, const int32_t* inv, const 
 // Sum of a token's expert rows, weighted or not.  U pieces of J rows are on their way
 // before the first sum.  Blocks an SM, by measurement: K = 2 wants many light threads (8:
 // 31.3 us, 6: 33.8, 5: 36.2 for 8192 x 2 rows of 4096 bf16), K = 8 few with all their loads
-// in flight (1: 24.2 us, the compiler's own choice 32.5, for 4096 x 8 rows of 2048 bf16).
+// in flight (1: 24.2 us, the compiler's own choice 32.5, for 4096 x 8 rows of 2048 bf16);
+// single values want 6 (4096 x 8 rows of 2047: 50 us, with 1 76).
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
+__global__ void __launch_bounds__(256, N == 1 ? 6 : K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
                                                            const float* __restrict__ w,
                                                            const int32_t* __restrict__ inv, int T_, int k, int cols,
                                                            T* __restrict__ y, int64_t ldy, int shift) {
@@ -365,6 +366,15 @@ __global__ void __launch_bounds__(256, K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows
   int rows[K];
   float wt[K];
   entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < K; ++j) any |= rows[j] >= 0;
+  if (!any) {  // a token behind the batch's end
+    const float zero[N] = {};
+    for (int c = blockIdx.y * at.P + at.lane; c < cols; c += gridDim.y * at.P)
+      store_vec<T, N>(y + at.t * ldy + (int64_t)c * N, zero);
+    return;
+  }
   for (int c = blockIdx.y * U * at.P + at.lane; c < cols; c += gridDim.y * U * at.P) {
     float acc[U][N] = {};
 #pragma unroll
@@ -398,7 +408,7 @@ __global__ void __launch_bounds__(256, K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows
 // 2048 x 2 rows of 4096 bf16: 16.0 us; 18.5 with one piece in flight, 18 to 19 with fewer
 // or more registers a thread.
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
+__global__ void __launch_bounds__(256, N == 1 ? (K <= 4 ? 6 : 4) : K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
                                                                const T* __restrict__ o, int64_t ldo,
                                                                const float* __restrict__ w,
                                                                const int32_t* __restrict__ inv, int T_, int k, int cols,
@@ -414,7 +424,10 @@ __global__ void __launch_bounds__(256, K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_back
   float wt[K], dot[K] = {};
   if (real) {
     entries_of<K>(at.t, inv, w, T_ * k, k, rows, wt);
-    for (int c = at.lane; c < cols; c += U * at.P) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < K; ++j) any |= rows[j] >= 0;
+    for (int c = any ? at.lane : cols; c < cols; c += U * at.P) {
       R g[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -530,12 +543,11 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
                         k, xsp, ldxs, n, shift);
 }
 
-// U: pieces of each row in flight, so that K * U loads of 16 bytes (single values: four
-// times as many) are, within 128 registers.
+// U: pieces of each row in flight.
 template <typename T, int N, int K>
 cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y,
                        cudaStream_t stream) {
-  constexpr int U = N == 1 ? 4 : 2;
+  constexpr int U = N == 1 && K <= 2 ? 4 : 2;
   const int cols = H / N, shift = walk_shift(cols, U, 256);
   const unsigned blocks = walk_blocks(T_, 256, shift);
   unsigned ny = 1;  // column blocks: more parallelism for few tokens
@@ -547,7 +559,7 @@ cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, 
 template <typename T, int N, int K>
 cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
                                 Rows d_o, float* dw, cudaStream_t stream) {
-  constexpr int U = N == 1 ? 4 : 2;
+  constexpr int U = N == 1 && K > 4 ? 4 : 2;
   const int cols = H / N;
   const int shift = walk_shift(cols, U, 256);
   return launch_chained(collect_backward_kernel<T, N, K, U>, dim3(walk_blocks(T_, 256, shift)), dim3(256), 0, stream,
