@@ -24,7 +24,6 @@
 
 namespace moe {
 
-constexpr int kSortSmall = 1024;   // entries that one launch sorts by counting
 constexpr int kSortBlock = 1024;
 constexpr int kSortMaxBlocks = 128;
 constexpr int kSortCluster = 8;    // blocks of the cluster that sorts more
@@ -34,31 +33,26 @@ static_assert(kMaxGroups <= kSortBlock, "the cluster's scan takes the keys in at
 
 __device__ __forceinline__ int sort_key(int32_t e, int E) { return (unsigned)e < (unsigned)E ? e : E; }
 
-// Copy one row of n units from src to dst; U is the widest unit that fits the pointers,
-// the pitches and the row.
-template <typename U>
-__device__ __forceinline__ void copy_row(const U* __restrict__ src, U* __restrict__ dst, int n) {
-  for (int c = threadIdx.x; c < n; c += blockDim.x) dst[c] = __ldg(src + c);
-}
-
-// Up to 1024 entries in one launch (2.1 us for 96 entries and rows of 4 KB): the row of entry
-// i is the number of entries with a smaller key plus that of equal keys before it, so each
-// block counts its own entry's row (every thread looks at up to four keys) and copies its
-// token's row there.  Block 0 makes the offsets.  At these sizes latency is all there is: one
-// launch instead of sort and gather behind one another.
-template <typename U>
+// Few entries in one launch: the row of an entry is the number of entries with a smaller
+// key, or an equal key and a smaller index, so each block counts its own token's rows (every
+// thread looks at its share of all keys) and copies the token's row there.  Key and index
+// are compared as one number.  Block 0 makes the offsets; blockIdx.y shares a long row.
+// At these sizes latency is all there is: 256 tokens x 8, rows of 4 KB, take 4.4 us, a sort and
+// the rows behind it 8.4 and a second launch on the host.  K: entries a token has at most.
+template <typename U, int K>
 __global__ void __launch_bounds__(256) dispatch_small_kernel(const int32_t* __restrict__ idx, int R, int k, int E,
                                                              int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                                                              int32_t* __restrict__ offsets, const U* __restrict__ x,
                                                              int64_t ldx, U* __restrict__ xs, int64_t ldxs, int n) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0) {
+    if (blockIdx.y != 0) return;
     __shared__ int32_t hist[kMaxGroups + 1];
     __shared__ int32_t wsum[8];
     for (int e = tid; e <= E; e += 256) hist[e] = 0;
     __syncthreads();
-    for (int i = tid; i < R; i += 256) atomicAdd(&hist[sort_key(idx[i], E)], 1);  // integer counts: any order
+    for (int i = tid; i < R; i += 256) atomicAdd(&hist[sort_key(__ldg(idx + i), E)], 1);  // integer counts: any order
     __syncthreads();
     int run = 0;
     for (int e0 = 0; e0 <= E; e0 += 256) {  // exclusive scan, 256 groups at a time
@@ -68,35 +62,62 @@ __global__ void __launch_bounds__(256) dispatch_small_kernel(const int32_t* __re
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, s, o);
-        if ((tid & 31) >= o) s += u;
+        if (lane >= o) s += u;
       }
-      if ((tid & 31) == 31) wsum[tid >> 5] = s;
+      if (lane == 31) wsum[warp] = s;
       __syncthreads();
       int before = run;
-      for (int w = 0; w < (tid >> 5); ++w) before += wsum[w];
+      for (int w = 0; w < warp; ++w) before += wsum[w];
       if (e <= E) offsets[e] = before + s - v;
       for (int w = 0; w < 8; ++w) run += wsum[w];
       __syncthreads();
     }
     return;
   }
-  const int i = blockIdx.x - 1;
-  const int key = sort_key(idx[i], E);
-  int row = 0;
-  for (int j0 = 0; j0 < R; j0 += 256) {
-    const int j = j0 + tid;
-    int before = 0;
-    if (j < R) {
-      const int kj = sort_key(idx[j], E);
-      before = kj < key || (kj == key && j < i);
+  __shared__ int32_t part[8][K];
+  const int t = blockIdx.x - 1, c0 = blockIdx.y * 256 + tid, cstep = gridDim.y * 256;
+  const U* src = x + (int64_t)t * ldx;
+  U piece{};
+  if (x && c0 < n) piece = __ldg(src + c0);  // on its way while the rows are counted
+  uint32_t own[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int i = t * k + j;
+    own[j] = j < k ? (uint32_t)sort_key(__ldg(idx + i), E) << 20 | (uint32_t)i : 0u;
+  }
+  int count[K] = {};
+#pragma unroll 4
+  for (int i = tid; i < R; i += 256) {
+    const uint32_t that = (uint32_t)sort_key(__ldg(idx + i), E) << 20 | (uint32_t)i;
+#pragma unroll
+    for (int j = 0; j < K; ++j) count[j] += that < own[j];
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    count[j] = __reduce_add_sync(0xffffffffu, count[j]);
+    if (lane == 0) part[warp][j] = count[j];
+  }
+  __syncthreads();
+  U* dst[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    int row = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) row += part[w][j];
+    const bool kept = j < k && (own[j] >> 20) < (uint32_t)E;
+    dst[j] = kept && x ? xs + (int64_t)row * ldxs : nullptr;
+    if (tid == j && j < k && blockIdx.y == 0) {
+      perm[row] = t * k + j;
+      inv[t * k + j] = kept ? row : -1;
     }
-    row += __syncthreads_count(before);
   }
-  if (tid == 0) {
-    perm[row] = i;
-    inv[i] = key < E ? row : -1;
+  if (!x) return;
+  for (int c = c0; c < n; c += cstep) {
+    const U v = c == c0 ? piece : __ldg(src + c);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (dst[j]) dst[j][c] = v;
   }
-  if (x && key < E) copy_row(x + (int64_t)(i / k) * ldx, xs + (int64_t)row * ldxs, n);
 }
 
 // Inclusive scan over a block of 1024 threads.  wsum: 32 words of shared memory.
@@ -514,6 +535,13 @@ cudaError_t sort_large(const int32_t* idx, int R, int E, int32_t* perm, int32_t*
                         (const int32_t*)hist, perm, inv, offsets);
 }
 
+// Whether the blocks count their rows themselves: up to 2^24 comparisons over all of them (512
+// tokens x 8: 8.5 us with rows of 4 KB where sort and rows take 9.6, 1024 x 8: 15.8 / 12.8),
+// without rows 2^23 (2048 entries 4.8 / 4.8 us, 4096 11.3 / 4.9).
+bool counts_rows(int T, int k, bool rows) {
+  return (int64_t)T * k * T * (k <= 2 ? 2 : k <= 4 ? 4 : 8) <= (rows ? 1 << 24 : 1 << 23);
+}
+
 // Threads that walk a row of n pieces, U at a time: a power of two from 8 to `most`, as its shift.
 int walk_shift(int n, int U, int most) {
   int s = 3;
@@ -531,9 +559,15 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
   const int n = (int)((int64_t)H * es / unit);
   const U* xp = (const U*)x.p;
   U* xsp = (U*)xs.p;
-  if (R <= kSortSmall)
-    return launch_chained(dispatch_small_kernel<U>, dim3(R + 1), dim3(256), 0, stream, idx, R, k, E, perm, inv, offsets,
-                          xp, ldx, xsp, ldxs, n);
+  if (counts_rows(T, k, xp != nullptr)) {
+    unsigned ny = 1;  // column blocks: more parallelism for few tokens
+    while (T * ny < 148 && (int64_t)ny * 256 < n) ny *= 2;
+    auto kern = k <= 2   ? dispatch_small_kernel<U, 2>
+                : k <= 4 ? dispatch_small_kernel<U, 4>
+                         : dispatch_small_kernel<U, 8>;
+    return launch_chained(kern, dim3(T + 1, ny), dim3(256), 0, stream, idx, R, k, E, perm, inv, offsets, xp, ldx, xsp,
+                          ldxs, n);
+  }
   cudaError_t e = R <= kSortMedium ? sort_medium(idx, R, E, perm, inv, offsets, stream)
                                    : sort_large(idx, R, E, perm, inv, offsets, (int32_t*)ws, stream);
   if (e != cudaSuccess || !xp) return e;

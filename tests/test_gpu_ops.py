@@ -81,7 +81,8 @@ def check_routes(r, idx, E):
 # ------------------------------------------------------------------ sort and dispatch
 @pytest.mark.parametrize("T,k,E,kind", [
     (0, 2, 8, "all"), (1, 1, 1, "all"), (1, 8, 8, "all"), (16, 6, 256, "all"), (33, 3, 5, "holes"),
-    (128, 8, 256, "padded"), (1024, 1, 1024, "outside"), (205, 5, 7, "holes"), (1025, 1, 1, "all"),
+    (128, 8, 256, "padded"), (1024, 1, 1024, "outside"), (205, 5, 7, "holes"), (1025, 1, 1, "all"), (2048, 1, 300, "holes"),
+    (2049, 1, 300, "holes"), (362, 8, 1024, "outside"), (363, 8, 256, "holes"), (1024, 2, 256, "padded"),
     (513, 2, 256, "none"), (700, 2, 64, "one"), (4097, 8, 256, "outside"), (8193, 1, 1023, "holes"),
     (3000, 3, 1024, "outside"), (16384, 1, 1024, "holes"), (16385, 1, 1024, "holes"), (16384, 3, 33, "holes"), (20000, 7, 1000, "padded"),
     (131072, 8, 128, "holes")])
@@ -93,7 +94,8 @@ def test_sort(T, k, E, kind):
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("T,k,E,H,kind", [
     (0, 2, 8, 64, "all"), (1, 1, 4, 1, "all"), (16, 6, 256, 2048, "all"), (37, 3, 5, 77, "holes"),
-    (200, 8, 64, 12, "outside"), (16385, 1, 1024, 24, "outside"), (8192, 6, 256, 64, "all"), (65536, 1, 3, 8, "padded"),
+    (200, 8, 64, 12, "outside"), (512, 8, 256, 40, "holes"), (513, 8, 256, 40, "holes"), (724, 4, 7, 24, "padded"),
+    (2048, 2, 8, 16, "holes"), (2, 5, 1024, 12288, "outside"), (16385, 1, 1024, 24, "outside"), (8192, 6, 256, 64, "all"), (65536, 1, 3, 8, "padded"),
     (5471, 3, 300, 33, "holes"), (8191, 8, 256, 40, "none"), (2731, 7, 77, 520, "one"), (13108, 5, 6, 16, "holes"), (1500, 2, 8, 130, "padded"), (300, 4, 16, 1001, "holes"), (400, 3, 9, 264, "none")])
 def test_dispatch(T, k, E, H, kind, dtype):
     idx, x = index(T, k, E, kind), rnd(T, H, dtype=dtype)
