@@ -590,32 +590,23 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
   }
   cluster_arrive();
   cluster_wait();
-  // P: the blocks' shares added in order, in 16-byte pieces; then split into hi and lo terms
-  constexpr int PIECES = RP / 4, EACH = TM * PIECES / kAdThreads;  // lanes of a row: a power of two up to 32
-  if (drains) {
-    constexpr int BATCH = 2;  // pieces, of up to four blocks, in flight
-    float4 sum[EACH] = {};
+  // P: the blocks' shares added in order, in 16-byte pieces, and split into hi and lo terms
+  constexpr int PIECES = RP / 4;  // lanes of a row, a power of two up to 32
+  if (drains)
+#pragma unroll 2
+    for (int c = tid; c < TM * PIECES; c += kAdThreads) {
+      const int row = c / PIECES, piece = c % PIECES;
+      float4 s = make_float4(0, 0, 0, 0);
+      if (piece * 4 < r && row < tile.rows) {  // the rank is a multiple of 8
+        float4 v[kAdMaxCluster];
 #pragma unroll
-    for (int i0 = 0; i0 < EACH; i0 += BATCH)
-      for (int b0 = 0; b0 < cluster; b0 += 4) {
-        float4 v[BATCH][4];
+        for (int k = 0; k < kAdMaxCluster; ++k)
+          if (k < cluster) v[k] = load_remote4(mine + c * 4, k);
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (b0 + b < cluster) v[i][b] = load_remote4(mine + (tid + (i0 + i) * kAdThreads) * 4, b0 + b);
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (b0 + b < cluster)
-              sum[i0 + i].x += v[i][b].x, sum[i0 + i].y += v[i][b].y, sum[i0 + i].z += v[i][b].z, sum[i0 + i].w += v[i][b].w;
+        for (int k = 0; k < kAdMaxCluster; ++k)
+          if (k < cluster) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+        s.x *= sc, s.y *= sc, s.z *= sc, s.w *= sc;
       }
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      const int c = tid + i * kAdThreads, row = c / PIECES, piece = c % PIECES;
-      const bool real = piece * 4 < r && row < tile.rows;  // the rank is a multiple of 8
-      float4 s = real ? make_float4(sum[i].x * sc, sum[i].y * sc, sum[i].z * sc, sum[i].w * sc) : make_float4(0, 0, 0, 0);
       if constexpr (is_f16<T>) {  // the row's lanes agree on its power of two
         uint32_t big = max(max(__float_as_uint(s.x) & 0x7FFFFFFFu, __float_as_uint(s.y) & 0x7FFFFFFFu),
                            max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
@@ -634,7 +625,6 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
       asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_hi + at), "r"(hi[0]), "r"(hi[1]) : "memory");
       asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_lo + at), "r"(lo[0]), "r"(lo[1]) : "memory");
     }
-  }
   cluster_arrive();  // this warp has read; no block may overwrite its share or leave before all have
   // the lane's outputs of a stage: eight in a row of two tokens
   const uint32_t at_y = swizzled(16 * m + g, 4 * half + q);  // eight rows further: 1024 bytes
