@@ -21,7 +21,7 @@
 // so a lane takes eight consecutive values, 16 bytes, of its row).  What bounds it is the
 // chain of latencies: finding the tile 0.8 us, loads and product 0.9, the cluster's meeting
 // 1.3, the second product 0.9.  K = N = 4096, r 16: 1 token 4.9 us, 64 requests of 48 adapters
-// 6.6 us; 64 requests of r 64 (69 MB of adapters) 12.2 us, 87% of the copy rate.
+// 6.6 us; 64 requests of r 64 (69 MB of adapters) 12.0 us, 89% of the copy rate.
 // Long batches: tiles of 64 tokens on tcgen05 (adapter_wide_kernel).  8192 tokens, K = N =
 // 2048, r 64 (113 MB): 31 us, 56% of the copy rate; r 128 43 us.  Each block goes through
 // finding its tile, the down product, the cluster's meeting and the up product once, all blocks
@@ -695,16 +695,18 @@ namespace {
 struct Shares {
   int tiles, cluster, kslice, nslice;
 };
-// tiles: an upper bound on the tiles of TM rows, of which often a fifth is there in fact.  A
-// tile gets blocks, each with at least a step of k or of outputs, while they stay within one and a half
-// times what the machine holds at once (per_sm: blocks an SM holds); 64-token tiles of 8192
-// tokens, r 64: 31.2 us with 2 blocks a tile, 37.6 with 1; r 128, one block an SM: 42.8 and
-// with 2 49.7.  16-token tiles get more where a block would read over `much` bytes of its
+// tiles: an upper bound on the tiles of TM rows; half of the last tiles of the adapters are
+// expected.  A tile gets blocks, each with at least a step of k or of outputs, while all fit
+// the machine at once (per_sm: blocks an SM holds): 64-token tiles of 8192 tokens of 24
+// adapters, r 64, take 31.2 us with 2 blocks a tile and 37.6 with 1; of 32 adapters, r 128, one
+// block an SM, 42.8 with 1 and 49.7 with 2; 2048 tokens of 16, r 64, 29.0 with 4 and 33.6 with 8,
+// more than fit.  16-token tiles get more where a block would read over `much` bytes of its
 // adapter: 1 MB over 4 blocks took 16.4 us, over 8 12.5.
 Shares shares_of(const AdapterArgs& a, int TM, int kstep, int per_sm, int64_t much) {
-  Shares s{(a.T < a.n ? a.T : a.n) + a.T / TM, 1, 0, 0};
+  const int most = a.T < a.n ? a.T : a.n, full = a.T / TM, likely = full + (most + 1) / 2;
+  Shares s{most + full, 1, 0, 0};
   auto more = [&] {
-    return 4 * s.tiles * s.cluster <= 3 * 148 * per_sm || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
+    return 2 * likely * s.cluster <= 148 * per_sm || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
   };
   while (s.cluster < kAdMaxCluster && std::max(a.K, a.N) > s.cluster * kstep && more()) s.cluster *= 2;
   s.kslice = ((a.K + s.cluster - 1) / s.cluster + 31) / 32 * 32;
