@@ -110,6 +110,13 @@ __device__ Tile find_tile(int want, int TM, const int32_t* __restrict__ offsets,
   return found;
 }
 
+// 16 bytes of y, which may be the output itself: not through the read-only path.
+__device__ __forceinline__ uint4 load_y16(const void* p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // out = y for the rows without an adapter, those from `first` on: a share of them for every
 // warp, whether its block has a tile or not.  The shares, 128 pieces of 16 bytes, start at the
 // last blocks, which have no tile if any has none.
@@ -142,6 +149,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   const float2 f = unpack2<T>(hi);
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
+
+// The power of two that brings a row of P, whose largest magnitude has these bits, into
+// [2^13, 2^14).  An infinity is taken for the largest finite value: it stays infinite, and the
+// finite terms beside it stay finite.
+__device__ __forceinline__ int exponent_beyond(uint32_t big) { return (int)(min(big, 0x7F7FFFFFu) >> 23) - 127 - 13; }
 
 // Eight values of a lane, its share of 32 of the rank, as the MMA's first operand (h: row g or
 // g + 8): pairs 0, 1 to the first MMA, 2, 3 to the second, as B's.
@@ -204,8 +216,8 @@ __device__ __forceinline__ void operand_p(const float* P, uint32_t (&hi)[KB][2][
         for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(p[b][i]) & 0x7FFFFFFFu);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-      if (big < 0x7F800000u && e > 0) {
+      const int e = exponent_beyond(big);
+      if (e > 0) {
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         back[h] = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(kAdThreads, NR <= 8 ? 2 : 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       v[h] = tok[h] >= 0 && nn + 8 * q < n1
-                 ? __ldg(reinterpret_cast<const uint4*>(y + (int64_t)tok[h] * ldy + nn + 8 * q))
+                 ? load_y16(y + (int64_t)tok[h] * ldy + nn + 8 * q)
                  : make_uint4(0, 0, 0, 0);
   };
   auto load_b = [&](int nn, int b, uint4 (&v)[4]) {
@@ -612,8 +624,8 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
                            max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
 #pragma unroll
         for (int o = PIECES / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-        const int e = (int)(big >> 23) - 127 - 13;  // 2^e: the row's largest is in [2^13, 2^14) after
-        const bool scaled = big < 0x7F800000u && e > 0;
+        const int e = exponent_beyond(big);
+        const bool scaled = e > 0;
         const float by = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
         s.x *= by, s.y *= by, s.z *= by, s.w *= by;
         if (piece == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;

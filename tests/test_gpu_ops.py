@@ -488,6 +488,22 @@ def test_adapters_beyond_half_range(T):
     assert adapters_near(moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, n)), want, mag, K, r, F16)
 
 
+@pytest.mark.parametrize("T,r", [(20, 8), (300, 128)])   # tiles of 16 and of 64 tokens
+def test_adapters_infinite_beside_large(T, r):
+    # a low-rank term beyond 32 bits next to one of 2^79, of the other sign: infinite as the
+    # formula's sum is, not the difference of two infinities
+    K, N = 64, 40
+    x, y = torch.zeros(T, K, dtype=F16, device="cuda"), rnd(T, N, dtype=F16)
+    x[:, 0], x[:, 1] = 2.0 ** 13, 2.0 ** -24
+    A, B = torch.zeros(1, r, K, dtype=F16, device="cuda"), torch.zeros(1, N, r, dtype=F16, device="cuda")
+    A[0, 0, 0], A[0, 1, 1] = 1.0, 2.0 ** -24
+    B[0, :, 0], B[0, :, 1] = 1.0, -1.0
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    ids[3] = -1
+    out = moe.moe_adapters(x, y, A, B, torch.full((1,), 2.0 ** 127, device="cuda"), moe.moe_sort(ids, 1))
+    assert bool((out[ids == 0] == float("inf")).all()) and torch.equal(out[3], y[3])
+
+
 @pytest.mark.parametrize("T,r", [(33, 8), (900, 40)])
 def test_adapters_keep_requests_apart(T, r):
     # one request's NaN and another's infinity stay in their rows
