@@ -160,6 +160,16 @@ void done(const char* name, moe_status rc) {
   throw Pending{};
 }
 
+// A call of the C ABI, during which other Python threads run: a launch waits where the
+// device's queue is full.
+template <typename F>
+void run(const char* name, F call) {
+  PyThreadState* held = PyEval_SaveThread();
+  const moe_status rc = call();
+  PyEval_RestoreThread(held);
+  done(name, rc);
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 // The caller's object if one was given, the new tensor otherwise.
 PyObject* answer(PyObject* given, const at::Tensor& t) {
@@ -244,7 +254,7 @@ PyObject* do_sort(PyObject* const* a) {
   THPObjectPtr hold(made);
   at::Tensor held;
   void* ws = c.workspace(a[5], need, held, &bytes);
-  done("moe_sort", moe_sort(ip, T, k, E, r.perm, r.inv, r.offsets, ws, bytes, nullptr, c.stream));
+  run("moe_sort", [&] { return moe_sort(ip, T, k, E, r.perm, r.inv, r.offsets, ws, bytes, nullptr, c.stream); });
   return hold.release();
 }
 
@@ -271,8 +281,10 @@ PyObject* do_dispatch(PyObject* const* a) {
   THPObjectPtr hold(made);
   at::Tensor held;
   void* ws = c.workspace(a[7], need, held, &bytes);
-  done("moe_dispatch", moe_dispatch(xr.p, xr.ld, dt, ip, T, k, E, H, xsr.p, xsr.ld, r.perm, r.inv, r.offsets, ws, bytes,
-                                    nullptr, c.stream));
+  run("moe_dispatch", [&] {
+    return moe_dispatch(xr.p, xr.ld, dt, ip, T, k, E, H, xsr.p, xsr.ld, r.perm, r.inv, r.offsets, ws, bytes, nullptr,
+                        c.stream);
+  });
   return Py_BuildValue("(NN)", answer(a[3], xs), hold.release());
 }
 
@@ -291,9 +303,10 @@ PyObject* collect(PyObject* const* a, bool weighted) {
   const at::Tensor y = c.given_or_empty(a[5], weighted ? "y" : "dx", {T, H}, o.scalar_type());
   const Rows yr = c.rows(y, weighted ? "y" : "dx", T, H, o.scalar_type());
   if (weighted)
-    done("moe_collect", moe_collect(r.p, r.ld, dt, w, inv, T, k, H, yr.p, yr.ld, c.stream));
+    run("moe_collect", [&] { return moe_collect(r.p, r.ld, dt, w, inv, T, k, H, yr.p, yr.ld, c.stream); });
   else
-    done("moe_dispatch_backward", moe_dispatch_backward(r.p, r.ld, dt, inv, T, k, H, yr.p, yr.ld, c.stream));
+    run("moe_dispatch_backward",
+        [&] { return moe_dispatch_backward(r.p, r.ld, dt, inv, T, k, H, yr.p, yr.ld, c.stream); });
   return answer(a[5], y);
 }
 PyObject* do_collect(PyObject* const* a) { return collect(a, true); }
@@ -315,8 +328,9 @@ PyObject* do_collect_backward(PyObject* const* a) {
   const at::Tensor dw = c.given_or_empty(a[7], "dw", {T, k}, at::kFloat);
   const Rows dr = c.rows(d, "do", R, H, o.scalar_type());
   float* dwp = (float*)c.flat(dw, "dw", R, at::kFloat);
-  done("moe_collect_backward", moe_collect_backward(gr.p, gr.ld, orw.p, orw.ld, dt, w, inv, T, k, H, dr.p, dr.ld, dwp,
-                                                    c.stream));
+  run("moe_collect_backward", [&] {
+    return moe_collect_backward(gr.p, gr.ld, orw.p, orw.ld, dt, w, inv, T, k, H, dr.p, dr.ld, dwp, c.stream);
+  });
   return Py_BuildValue("(NN)", answer(a[6], d), answer(a[7], dw));
 }
 
@@ -334,7 +348,8 @@ PyObject* do_act_save(PyObject* const* a) {
   if (!fresh) k = ckpt(c, a[1], R, F);
   THPObjectPtr handle(fresh ? new_handle(c.empty({ckpt_bytes(R, F)}, at::kByte), 0, R, F, &k) : Py_NewRef(a[1]));
   if (!handle) throw Pending{};
-  done("moe_act_save", moe_act_save(r.p, r.ld, dt, R, F, k.q, k.e, c.limit(a[2]), c.stream));
+  const int32_t* limit = c.limit(a[2]);
+  run("moe_act_save", [&] { return moe_act_save(r.p, r.ld, dt, R, F, k.q, k.e, limit, c.stream); });
   return handle.release();
 }
 
@@ -349,7 +364,8 @@ PyObject* do_act_load(PyObject* const* a) {
   const int32_t dt = value_type(x, "x");
   const Rows r = c.rows(x, "x", R, F, x.scalar_type());
   const Ckpt k = ckpt(c, a[0], R, F);
-  done("moe_act_load", moe_act_load(k.q, k.e, R, F, dt, r.p, r.ld, c.limit(a[3]), c.stream));
+  const int32_t* limit = c.limit(a[3]);
+  run("moe_act_load", [&] { return moe_act_load(k.q, k.e, R, F, dt, r.p, r.ld, limit, c.stream); });
   return answer(a[2], x);
 }
 
@@ -377,8 +393,10 @@ PyObject* do_swiglu_save(PyObject* const* a) {
   }
   if (!made) throw Pending{};
   THPObjectPtr handles(made);
-  done("moe_swiglu_save", moe_swiglu_save(gr.p, gr.ld, ur.p, ur.ld, dt, R, F, hr.p, hr.ld, kg.q, kg.e, ku.q, ku.e,
-                                          c.limit(a[4]), c.stream));
+  const int32_t* limit = c.limit(a[4]);
+  run("moe_swiglu_save", [&] {
+    return moe_swiglu_save(gr.p, gr.ld, ur.p, ur.ld, dt, R, F, hr.p, hr.ld, kg.q, kg.e, ku.q, ku.e, limit, c.stream);
+  });
   return Py_BuildValue("(NN)", answer(a[2], h), handles.release());
 }
 
@@ -398,8 +416,11 @@ PyObject* do_swiglu_backward(PyObject* const* a) {
   const at::Tensor h = again ? c.given_or_empty(a[4], "h", {R, F}, type) : at::Tensor();
   const Rows gr = c.rows(dg, "dg", R, F, type), ur = c.rows(du, "du", R, F, type);
   const Rows hr = again ? c.rows(h, "h", R, F, type) : Rows{nullptr, F};
-  done("moe_swiglu_backward", moe_swiglu_backward(r.p, r.ld, dt, kg.q, kg.e, ku.q, ku.e, R, F, gr.p, gr.ld, ur.p, ur.ld,
-                                                  hr.p, hr.ld, c.limit(a[6]), c.stream));
+  const int32_t* limit = c.limit(a[6]);
+  run("moe_swiglu_backward", [&] {
+    return moe_swiglu_backward(r.p, r.ld, dt, kg.q, kg.e, ku.q, ku.e, R, F, gr.p, gr.ld, ur.p, ur.ld, hr.p, hr.ld, limit,
+                               c.stream);
+  });
   return Py_BuildValue("(NNN)", answer(a[2], dg), answer(a[3], du), again ? answer(a[4], h) : Py_NewRef(Py_None));
 }
 
@@ -424,8 +445,10 @@ PyObject* do_adapters(PyObject* const* a) {
   const at::Tensor out = c.given_or_empty(a[11], "out", {T, N}, type);
   const Rows outr = c.rows(out, "out", T, N, type);
   int32_t* status = none(a[12]) ? nullptr : (int32_t*)c.flat(a[12], "status", 1, at::kInt);
-  done("moe_adapters", moe_adapters(xr.p, xr.ld, yr.p, yr.ld, dt, T, K, N, r, n, Ap, Bp, scale, rt.perm, rt.offsets, outr.p,
-                                    outr.ld, status, c.stream));
+  run("moe_adapters", [&] {
+    return moe_adapters(xr.p, xr.ld, yr.p, yr.ld, dt, T, K, N, r, n, Ap, Bp, scale, rt.perm, rt.offsets, outr.p, outr.ld,
+                        status, c.stream);
+  });
   return answer(a[11], out);
 }
 
