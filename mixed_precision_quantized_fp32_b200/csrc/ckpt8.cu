@@ -18,10 +18,11 @@
 // Memory bounds all of these.  A quad of lanes takes one group, eight values a lane, so
 // bf16 loads are 16 bytes and code stores 8 bytes a lane, consecutive over the warp, and
 // the group's maximum takes two shuffles.  Rows whose pitch or start does not allow that
-// run with one value a lane and group.  Of the measured copy rate:
+// run with fewer values a lane.  Of the measured copy rate:
 //   save and load, 8192 x 4096 bf16 (203 MB)               31.2 us, 101%
 //   SwiGLU forward and backward, 4096 x 14336 bf16 (1.06 GB)  162 us, 102%
-//   the same with one value a lane: 8192 x 4095 73 us, 43%; 4096 x 5001 115 us, 50%
+//   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 46, 50, 68 us
+//   (69, 63, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 81, 114 us (81, 71, 50%)
 #include <initializer_list>
 
 #include "ops_common.cuh"
@@ -55,25 +56,33 @@ __device__ __forceinline__ uint32_t code_bits(float x, float inv) {
 }
 __device__ __forceinline__ float clamp127(float x) { return fminf(fmaxf(x, -127.0f), 127.0f); }
 
-// Codes of eight values.  Only the highest exponent can leave values beyond 127 steps, and
-// only 255 stands for values without codes: both take the branch.
-template <typename T>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t eb) {
-  uint32_t c[8];
+// Codes of N values, up to four in a word.  Only the highest exponent can leave values beyond 127
+// steps, and only 255 stands for values without codes: both take the branch.
+template <typename T, int N>
+__device__ __forceinline__ void encode(const float (&v)[N], uint32_t eb, uint32_t (&q)[(N + 3) / 4]) {
+  uint32_t c[N];
   if (eb < (uint32_t)(emax<T>() + 127)) {
     const float inv = inv_step(eb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = code_bits(v[i], inv);
+    for (int i = 0; i < N; ++i) c[i] = code_bits(v[i], inv);
   } else {
-    if (eb == 255u) return make_uint2(0u, 0u);
     const float inv = inv_step(eb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = code_bits(clamp127(v[i] * inv), 1.0f);
+    for (int i = 0; i < N; ++i) c[i] = eb == 255u ? 0u : code_bits(clamp127(v[i] * inv), 1.0f);
   }
-  uint2 q;
-  q.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-  q.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-  return q;
+  if constexpr (N < 4) {
+    q[0] = N == 1 ? c[0] & 0xFFu : __byte_perm(c[0], c[N - 1], 0x4440) & 0xFFFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      q[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t eb) {
+  uint32_t q[2];
+  encode<T, 8>(v, eb, q);
+  return make_uint2(q[0], q[1]);
 }
 
 // Eight values as they lie in memory.
@@ -118,22 +127,29 @@ __device__ __forceinline__ uint32_t quad_amax(const Eight<T>& e) {
   }
 }
 
-// q * 2^e of eight codes.  One byte permute makes 2^23 + 128 + q as a float, one fused
+// q * 2^e of N codes.  One byte permute makes 2^23 + 128 + q as a float, one fused
 // multiply-add takes the offset off and scales; both are exact.  Steps of 2^103 and more,
 // where the offset times the step would overflow, and NaN groups multiply afterwards.
-__device__ __forceinline__ void decode8(uint2 q, uint32_t eb, float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void decode(const uint32_t (&q)[(N + 3) / 4], uint32_t eb, float (&v)[N]) {
   const float step = step_of(eb);
-  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  uint32_t w[(N + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < (N + 3) / 4; ++i) w[i] = q[i] ^ 0x80808080u;
   if (eb < 230u) {
     const float off = -8388736.0f * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
       v[i] = fmaf(__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7440 + i % 4)), step, off);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
       v[i] = (__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7440 + i % 4)) - 8388736.0f) * step;
   }
+}
+__device__ __forceinline__ void decode8(uint2 c, uint32_t eb, float (&v)[8]) {
+  const uint32_t q[2] = {c.x, c.y};
+  decode<8>(q, eb, v);
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
@@ -316,202 +332,301 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(
   }
 }
 
-// ---------------------------------------------------------------- one value a lane
-// Any width, pitch and alignment: a warp takes S consecutive groups of a row, one value of
-// each a lane, so that loads and stores are consecutive over the warp and S of them are in
-// flight, and the row is found once for 32 S values.
-constexpr int kSpan = 8;       // groups a warp of save and load takes
-constexpr int kSpanSwiglu = 4; // of the SwiGLU kernels, which read two or three matrices
+// ---------------------------------------------------------------- fewer values a lane
+// Any width, pitch and alignment: a lane has N consecutive values in accesses of V (4, 2 or 1,
+// what widths, rows and codes are aligned to; N >= V).  A warp takes N groups of a row at once,
+// S times, with all loads in flight, and finds the row once.  The number of instructions bounds
+// these kernels, so what a group needs once is shared by few lanes, as far as the accesses then
+// leave the bytes between them to the next: single values, save and load of 8192 x 4095 bf16,
+// take 68 us with N = 2 (1: 76, 4: 71); the SwiGLU kernels, with more to do for a value, 114 for
+// 4096 x 5001 with N = 1 (4: 135).  Pairs take N = 4: 50 us where N = 2 took 58.
+template <int V> constexpr int kMany = V == 1 ? 2 : 4;  // N of save and load
+template <int V> constexpr int kSpan = 8 / kMany<V>;    // their S
+template <int V> constexpr int kFew = V == 1 ? 1 : 4;   // N of the SwiGLU kernels
 
-// The warp's groups [grp, grp + S) of row `row`, its lane's first column and what is left of
-// the row from there.
+// The lane's first group and column and what is left of the row from there; its next group
+// lies N groups further.
 struct Span {
   int64_t row;
   int grp, col, left;
-  bool in;
+  bool in;  // the warp has a row
 };
-template <int S>
+template <int N, int S>
 __device__ __forceinline__ Span span_of(int G, int rows, int F) {
-  const uint32_t spans = (uint32_t)(G + S - 1) / S, at = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const uint32_t row = at / spans;
+  const uint32_t spans = (uint32_t)(G + N * S - 1) / (N * S), at = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const uint32_t row = at / spans, lane = threadIdx.x & 31;
   Span s;
   s.row = row;
-  s.grp = (int)(at - row * spans) * S;
-  s.col = s.grp * kGroup + (threadIdx.x & 31);
+  s.grp = (int)(at - row * spans) * N * S;
+  s.col = s.grp * kGroup + lane * N;
+  s.grp += lane * N / kGroup;
   s.left = F - s.col;
   s.in = row < (uint32_t)rows;
   return s;
 }
 
-template <typename T, int S>
-__device__ __forceinline__ void load_span(const T* __restrict__ p, int left, float (&v)[S]) {
-#pragma unroll
-  for (int i = 0; i < S; ++i) v[i] = i * kGroup < left ? to_f32<T>(__ldg(p + i * kGroup)) : 0.0f;
+// V values at p, zeros where there are none.
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, bool in, float* v) {
+  if constexpr (V == 1) {
+    v[0] = in ? to_f32<T>(__ldg(p)) : 0.0f;
+  } else if constexpr (sizeof(T) * V == 16) {
+    const float4 f = in ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[0] = f.x, v[1] = f.y, v[V - 2] = f.z, v[V - 1] = f.w;
+  } else if constexpr (sizeof(T) == 4) {
+    const float2 f = in ? __ldg(reinterpret_cast<const float2*>(p)) : make_float2(0.0f, 0.0f);
+    v[0] = f.x, v[1] = f.y;
+  } else if constexpr (V == 2) {
+    const float2 f = unpack2<T>(in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+    const uint2 q = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
+    const float2 f = unpack2<T>(q.x), g = unpack2<T>(q.y);
+    v[0] = f.x, v[1] = f.y, v[V - 2] = g.x, v[V - 1] = g.y;
+  }
 }
-template <typename T, int S>
-__device__ __forceinline__ void store_span(T* p, int left, const float (&v)[S]) {
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float* v) {
+  if constexpr (V == 1) *p = from_f32<T>(v[0]);
+  else if constexpr (sizeof(T) * V == 16) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[V - 2], v[V - 1]);
+  else if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = pack2<T>(v[0], v[1]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[V - 2], v[V - 1]));
+}
+template <int V> struct CodesOf;
+template <> struct CodesOf<1> { using type = uint8_t; };
+template <> struct CodesOf<2> { using type = uint16_t; };
+template <> struct CodesOf<4> { using type = uint32_t; };
+
+// A span's values from p on, zeros behind the row's end, and back.
+template <int V, typename T, int N, int S>
+__device__ __forceinline__ void load_span(const T* p, int left, float (&v)[S][N]) {
 #pragma unroll
   for (int i = 0; i < S; ++i)
-    if (i * kGroup < left) p[i * kGroup] = from_f32<T>(v[i]);
+#pragma unroll
+    for (int j = 0; j < N; j += V) load_v<T, V>(p + i * N * kGroup + j, i * N * kGroup + j < left, v[i] + j);
+}
+template <int V, typename T, int N, int S>
+__device__ __forceinline__ void store_span(T* p, int left, const float (&v)[S][N]) {
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < N; j += V)
+      if (i * N * kGroup + j < left) store_v<T, V>(p + i * N * kGroup + j, v[i] + j);
 }
 
-// Codes and exponents of the warp's groups; the first S lanes store one exponent each.
-template <typename T, int S>
-__device__ __forceinline__ void encode_span(const float (&v)[S], int left, int groups, int8_t* q, uint8_t* ex) {
+// A span's codes and exponents; a group's largest value is found by its 32 / N lanes.
+template <typename T, int V, int N, int S>
+__device__ __forceinline__ void encode_span(const float (&v)[S][N], int left, int8_t* q, uint8_t* ex) {
+  using C = typename CodesOf<V>::type;
   const int lane = threadIdx.x & 31;
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < S; ++i) {
-    const uint32_t eb = group_exp<T>(__reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu));
-    if (lane == i) mine = eb;
-    if (i * kGroup < left)
-      q[i * kGroup] = eb == 255u ? (int8_t)0 : (int8_t)(code_bits(clamp127(v[i] * inv_step(eb)), 1.0f) & 0xFFu);
+    uint32_t m = 0, c[1];
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+    if constexpr (N == 1) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+      for (int o = 1; o < 32 / N; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const uint32_t eb = group_exp<T>(m);
+    encode<T, N>(v[i], eb, c);
+#pragma unroll
+    for (int j = 0; j < N; j += V)
+      if (i * N * kGroup + j < left) *reinterpret_cast<C*>(q + i * N * kGroup + j) = (C)(c[0] >> (8 * j));
+    if (N > 1 && lane % (32 / N) == 0 && i * N * kGroup < left) ex[N * i] = (uint8_t)eb;
+    if (N == 1 && lane == i) mine = eb;
   }
-  if (lane < S && lane < groups) ex[lane] = (uint8_t)mine;
+  // single values: the first S lanes store one each (left counts from column `lane` on)
+  if (N == 1 && lane < S && lane * kGroup < left + lane) ex[lane] = (uint8_t)mine;
 }
-template <int S>
-__device__ __forceinline__ void decode_span(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex, int left,
-                                            int groups, float (&v)[S]) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t mine = lane < S && lane < groups ? __ldg(ex + lane) : 0u;
+template <int V, int N, int S>
+__device__ __forceinline__ void load_codes(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex, int left,
+                                           uint32_t (&c)[S][1], uint32_t (&eb)[S]) {
+  using C = typename CodesOf<V>::type;
 #pragma unroll
-  for (int i = 0; i < S; ++i) v[i] = i * kGroup < left ? (float)__ldg(q + i * kGroup) : 0.0f;
+  for (int i = 0; i < S; ++i) {
+    c[i][0] = 0;
 #pragma unroll
-  for (int i = 0; i < S; ++i) v[i] *= step_of(__shfl_sync(0xffffffffu, mine, i));
+    for (int j = 0; j < N; j += V)
+      if (i * N * kGroup + j < left)
+        c[i][0] |= (uint32_t)__ldg(reinterpret_cast<const C*>(q + i * N * kGroup + j)) << (8 * j);
+    eb[i] = i * N * kGroup < left ? __ldg(ex + N * i) : 0u;
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) act_save1_kernel(const T* __restrict__ x, int64_t ldx, int R, int F,
-                                                        int8_t* __restrict__ q, uint8_t* __restrict__ ex,
-                                                        const int32_t* __restrict__ n_rows) {
+template <typename T, int V>
+__global__ void __launch_bounds__(256) act_save_v_kernel(const T* __restrict__ x, int64_t ldx, int R, int F,
+                                                         int8_t* __restrict__ q, uint8_t* __restrict__ ex,
+                                                         const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
+  constexpr int N = kMany<V>, S = kSpan<V>;
   const int G = (F + kGroup - 1) / kGroup;
-  const Span s = span_of<kSpan>(G, row_count(R, n_rows), F);
+  const Span s = span_of<N, S>(G, row_count(R, n_rows), F);
   if (!s.in) return;
-  float v[kSpan];
-  load_span<T>(x + s.row * ldx + s.col, s.left, v);
-  encode_span<T>(v, s.left, G - s.grp, q + s.row * F + s.col, ex + s.row * G + s.grp);
+  float v[S][N];
+  load_span<V>(x + s.row * ldx + s.col, s.left, v);
+  encode_span<T, V>(v, s.left, q + s.row * F + s.col, ex + s.row * G + s.grp);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) act_load1_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex,
-                                                        int R, int F, T* __restrict__ x, int64_t ldx,
-                                                        const int32_t* __restrict__ n_rows) {
+template <typename T, int V>
+__global__ void __launch_bounds__(256) act_load_v_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ ex,
+                                                         int R, int F, T* __restrict__ x, int64_t ldx,
+                                                         const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
+  constexpr int N = kMany<V>, S = kSpan<V>;
   const int G = (F + kGroup - 1) / kGroup;
-  const Span s = span_of<kSpan>(G, row_count(R, n_rows), F);
+  const Span s = span_of<N, S>(G, row_count(R, n_rows), F);
   if (!s.in) return;
-  float v[kSpan];
-  decode_span(q + s.row * F + s.col, ex + s.row * G + s.grp, s.left, G - s.grp, v);
-  store_span<T>(x + s.row * ldx + s.col, s.left, v);
+  uint32_t c[S][1], eb[S];
+  load_codes<V, N>(q + s.row * F + s.col, ex + s.row * G + s.grp, s.left, c, eb);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    float v[1][N];
+    decode<N>(c[i], eb[i], v[0]);
+    store_span<V>(x + s.row * ldx + s.col + i * N * kGroup, s.left - i * N * kGroup, v);
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) swiglu_save1_kernel(const T* __restrict__ g, int64_t ldg,
-                                                           const T* __restrict__ u, int64_t ldu, int R, int F,
-                                                           T* __restrict__ h, int64_t ldh, int8_t* __restrict__ gq,
-                                                           uint8_t* __restrict__ ge, int8_t* __restrict__ uq,
-                                                           uint8_t* __restrict__ ue,
-                                                           const int32_t* __restrict__ n_rows) {
+template <typename T, int V, int S>
+__global__ void __launch_bounds__(256) swiglu_save_v_kernel(const T* __restrict__ g, int64_t ldg,
+                                                            const T* __restrict__ u, int64_t ldu, int R, int F,
+                                                            T* __restrict__ h, int64_t ldh, int8_t* __restrict__ gq,
+                                                            uint8_t* __restrict__ ge, int8_t* __restrict__ uq,
+                                                            uint8_t* __restrict__ ue,
+                                                            const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
+  constexpr int N = kFew<V>;
   const int G = (F + kGroup - 1) / kGroup;
-  const Span s = span_of<kSpanSwiglu>(G, row_count(R, n_rows), F);
+  const Span s = span_of<N, S>(G, row_count(R, n_rows), F);
   if (!s.in) return;
-  float a[kSpanSwiglu], b[kSpanSwiglu];
-  load_span<T>(g + s.row * ldg + s.col, s.left, a);
-  load_span<T>(u + s.row * ldu + s.col, s.left, b);
+  float a[S][N], b[S][N];
+  load_span<V>(g + s.row * ldg + s.col, s.left, a);
+  load_span<V>(u + s.row * ldu + s.col, s.left, b);
   const int64_t at = s.row * F + s.col, e_at = s.row * G + s.grp;
-  encode_span<T>(a, s.left, G - s.grp, gq + at, ge + e_at);
-  encode_span<T>(b, s.left, G - s.grp, uq + at, ue + e_at);
+  encode_span<T, V>(a, s.left, gq + at, ge + e_at);
+  encode_span<T, V>(b, s.left, uq + at, ue + e_at);
 #pragma unroll
-  for (int i = 0; i < kSpanSwiglu; ++i) a[i] = swiglu(a[i], b[i]);
-  store_span<T>(h + s.row * ldh + s.col, s.left, a);
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[i][j] = swiglu(a[i][j], b[i][j]);
+  store_span<V>(h + s.row * ldh + s.col, s.left, a);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) swiglu_backward1_kernel(
+template <typename T, int V, int S>
+__global__ void __launch_bounds__(256) swiglu_backward_v_kernel(
     const T* __restrict__ dh, int64_t lddh, const int8_t* __restrict__ gq, const uint8_t* __restrict__ ge,
     const int8_t* __restrict__ uq, const uint8_t* __restrict__ ue, int R, int F, T* __restrict__ dg, int64_t lddg,
     T* __restrict__ du, int64_t lddu, T* __restrict__ h, int64_t ldh, const int32_t* __restrict__ n_rows) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
+  constexpr int N = kFew<V>;
   const int G = (F + kGroup - 1) / kGroup;
-  const Span s = span_of<kSpanSwiglu>(G, row_count(R, n_rows), F);
+  const Span s = span_of<N, S>(G, row_count(R, n_rows), F);
   if (!s.in) return;
   const int64_t at = s.row * F + s.col, e_at = s.row * G + s.grp;
-  float d[kSpanSwiglu], a[kSpanSwiglu], b[kSpanSwiglu];
-  load_span<T>(dh + s.row * lddh + s.col, s.left, d);
-  decode_span(gq + at, ge + e_at, s.left, G - s.grp, a);
-  decode_span(uq + at, ue + e_at, s.left, G - s.grp, b);
+  float d[S][N], a[S][N], b[S][N];
+  uint32_t cg[S][1], cu[S][1], eg[S], eu[S];
+  load_span<V>(dh + s.row * lddh + s.col, s.left, d);
+  load_codes<V, N>(gq + at, ge + e_at, s.left, cg, eg);
+  load_codes<V, N>(uq + at, ue + e_at, s.left, cu, eu);
 #pragma unroll
-  for (int i = 0; i < kSpanSwiglu; ++i) {
-    const Grads r = swiglu_grad(a[i], b[i], d[i]);
-    d[i] = r.dg, a[i] = r.du, b[i] = r.h;
+  for (int i = 0; i < S; ++i) {
+    decode<N>(cg[i], eg[i], a[i]);
+    decode<N>(cu[i], eu[i], b[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const Grads r = swiglu_grad(a[i][j], b[i][j], d[i][j]);
+      d[i][j] = r.dg, a[i][j] = r.du, b[i][j] = r.h;
+    }
   }
-  store_span<T>(dg + s.row * lddg + s.col, s.left, d);
-  store_span<T>(du + s.row * lddu + s.col, s.left, a);
-  if (h) store_span<T>(h + s.row * ldh + s.col, s.left, b);
+  store_span<V>(dg + s.row * lddg + s.col, s.left, d);
+  store_span<V>(du + s.row * lddu + s.col, s.left, a);
+  if (h) store_span<V>(h + s.row * ldh + s.col, s.left, b);
 }
 
 // ---------------------------------------------------------------- host
 namespace {
 
-// How a call runs: one value a lane, eight, or eight with all rows in one.
-enum class Way { kOne, kEight, kFlat };
+// How a call runs: one, two, four or eight values a lane, or eight with all rows in one.
+enum class Way { kOne, kTwo, kFour, kEight, kFlat };
 
 struct Matrix {
   const void* p;
   int64_t ld;
 };
-// Eight values a lane need 16-byte rows and codes on 8-byte boundaries.
+// The widest that widths, rows (in values of es bytes) and codes allow.  Eight values want
+// rows on 16 bytes and codes on 8.
 Way way_of(int es, int F, std::initializer_list<Matrix> rows, std::initializer_list<const void*> codes) {
-  bool eight = F % 8 == 0, flat = F % kGroup == 0;
+  uint64_t bytes = 0, values = (uint64_t)F;
+  bool flat = F % kGroup == 0;
   for (const Matrix& m : rows) {
     if (!m.p) continue;
-    eight = eight && on16(m.p) && (m.ld * es) % 16 == 0;
+    bytes |= (uint64_t)(uintptr_t)m.p | (uint64_t)(m.ld * es);
     flat = flat && m.ld == F;
   }
-  for (const void* c : codes) eight = eight && ((uintptr_t)c & 7) == 0;
-  return !eight ? Way::kOne : flat ? Way::kFlat : Way::kEight;
+  for (const void* c : codes) values |= (uint64_t)(uintptr_t)c;
+  auto allow = [&](int v) { return values % v == 0 && bytes % (v * es < 16 ? v * es : 16) == 0; };
+  if (allow(8)) return flat ? Way::kFlat : Way::kEight;
+  return allow(4) ? Way::kFour : allow(2) ? Way::kTwo : Way::kOne;
 }
 
-// span: groups a warp of the one-value kernel takes.
+// span: groups a warp takes where it has fewer than eight values a lane.
 dim3 grid_of(Way w, int R, int F, int span) {
   const uint64_t G = (F + kGroup - 1) / kGroup;
-  if (w == Way::kOne) return dim3((unsigned)((R * ((G + span - 1) / span) + 7) / 8));
+  if (w < Way::kEight) return dim3((unsigned)((R * ((G + span - 1) / span) + 7) / 8));
   return dim3((unsigned)((R * G + kGroupsPerBlock - 1) / kGroupsPerBlock));
 }
 
-#define MOE_PICK(w, name, T) \
-  ((w) == Way::kOne ? name##1_kernel<T> : (w) == Way::kFlat ? name##_kernel<T, true> : name##_kernel<T, false>)
+// SwiGLU of pairs and fours: S = 2 where there are groups enough for all warps the machine holds
+// (4096 x 5002 bf16 81 us, S = 1 92), else 1 (1000 x 1022 7.3 us, S = 2 8.4; 333 x 778 fp32 4.3 / 5.0).
+bool long_spans(int R, int F) { return (int64_t)R * ((F + kGroup - 1) / kGroup) >= 1 << 17; }
+int swiglu_span(Way w, int R, int F) { return w == Way::kOne || !long_spans(R, F) ? 4 : 8; }
+
+#define MOE_PICK(w, name, T)                          \
+  ((w) == Way::kOne     ? name##_v_kernel<T, 1>        \
+   : (w) == Way::kTwo   ? name##_v_kernel<T, 2>        \
+   : (w) == Way::kFour  ? name##_v_kernel<T, 4>        \
+   : (w) == Way::kEight ? name##_kernel<T, false>     \
+                        : name##_kernel<T, true>)
+#define MOE_PICK_SWIGLU(w, many, name, T)                                             \
+  ((w) == Way::kOne     ? name##_v_kernel<T, 1, 4>                                     \
+   : (w) == Way::kTwo   ? ((many) ? name##_v_kernel<T, 2, 2> : name##_v_kernel<T, 2, 1>) \
+   : (w) == Way::kFour  ? ((many) ? name##_v_kernel<T, 4, 2> : name##_v_kernel<T, 4, 1>) \
+   : (w) == Way::kEight ? name##_kernel<T, false>                                     \
+                        : name##_kernel<T, true>)
 
 template <typename T>
 cudaError_t save_as(ConstRows x, int R, int F, Ckpt c, const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
-  return launch_chained(MOE_PICK(w, act_save, T), grid_of(w, R, F, kSpan), dim3(256), 0, s, (const T*)x.p, x.ld, R, F, c.q, c.e,
+  return launch_chained(MOE_PICK(w, act_save, T), grid_of(w, R, F, 8), dim3(256), 0, s, (const T*)x.p, x.ld, R, F, c.q, c.e,
                         n_rows);
 }
 template <typename T>
 cudaError_t load_as(Ckpt c, int R, int F, Rows x, const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{x.p, x.ld}}, {c.q});
-  return launch_chained(MOE_PICK(w, act_load, T), grid_of(w, R, F, kSpan), dim3(256), 0, s, (const int8_t*)c.q,
+  return launch_chained(MOE_PICK(w, act_load, T), grid_of(w, R, F, 8), dim3(256), 0, s, (const int8_t*)c.q,
                         (const uint8_t*)c.e, R, F, (T*)x.p, x.ld, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_save_as(ConstRows g, ConstRows u, int R, int F, Rows h, Ckpt cg, Ckpt cu, const int32_t* n_rows,
                            cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{g.p, g.ld}, {u.p, u.ld}, {h.p, h.ld}}, {cg.q, cu.q});
-  return launch_chained(MOE_PICK(w, swiglu_save, T), grid_of(w, R, F, kSpanSwiglu), dim3(256), 0, s, (const T*)g.p, g.ld,
+  return launch_chained(MOE_PICK_SWIGLU(w, long_spans(R, F), swiglu_save, T), grid_of(w, R, F, swiglu_span(w, R, F)), dim3(256), 0, s, (const T*)g.p, g.ld,
                         (const T*)u.p, u.ld, R, F, (T*)h.p, h.ld, cg.q, cg.e, cu.q, cu.e, n_rows);
 }
 template <typename T>
 cudaError_t swiglu_backward_as(ConstRows dh, Ckpt cg, Ckpt cu, int R, int F, Rows dg, Rows du, Rows h,
                                const int32_t* n_rows, cudaStream_t s) {
   const Way w = way_of(sizeof(T), F, {{dh.p, dh.ld}, {dg.p, dg.ld}, {du.p, du.ld}, {h.p, h.ld}}, {cg.q, cu.q});
-  return launch_chained(MOE_PICK(w, swiglu_backward, T), grid_of(w, R, F, kSpanSwiglu), dim3(256), 0, s, (const T*)dh.p, dh.ld,
+  return launch_chained(MOE_PICK_SWIGLU(w, long_spans(R, F), swiglu_backward, T), grid_of(w, R, F, swiglu_span(w, R, F)), dim3(256), 0, s, (const T*)dh.p, dh.ld,
                         (const int8_t*)cg.q, (const uint8_t*)cg.e, (const int8_t*)cu.q, (const uint8_t*)cu.e, R, F,
                         (T*)dg.p, dg.ld, (T*)du.p, du.ld, (T*)h.p, h.ld, n_rows);
 }
 #undef MOE_PICK
+#undef MOE_PICK_SWIGLU
 
 }  // namespace
 

@@ -396,6 +396,43 @@ def test_swiglu_not_finite():
     assert torch.equal(torch.isnan(du), bad) and torch.equal(torch.isnan(dg), bad | ubad)
 
 
+# widths, pitches and offsets in fours, in pairs and odd: accesses of 4, 2 and 1 values
+@pytest.mark.parametrize("F,pitch,offset", [(260, 260, 0), (256, 260, 4), (28, 36, 8), (258, 258, 0), (256, 258, 2), (26, 40, 8),
+                                            (260, 266, 4), (1, 2, 1), (2, 2, 0), (4, 4, 0), (33, 33, 0), (510, 513, 3)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_checkpoint_in_fours_pairs_and_singles(F, pitch, offset, dtype):
+    test_checkpoint_through_views_and_row_limits(F, pitch, offset, dtype)
+    test_checkpoint_is_exact(9, F, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("R,F", [(6, 2), (9, 12), (7, 30), (20, 258), (20, 260), (3, 1022), (40, 67)])
+def test_swiglu_in_fours_pairs_and_singles(R, F, dtype):
+    test_swiglu_with_checkpoint(R, F, dtype)
+
+
+@pytest.mark.parametrize("F,gap", [(260, 0), (260, 2), (260, 1), (258, 4), (258, 1), (36, 4)])
+def test_swiglu_halves_in_fours_pairs_and_singles(F, gap):
+    test_swiglu_on_halves_of_one_matrix_with_row_limit(F, gap)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("F", [1921, 1922, 1924])
+def test_swiglu_of_many_rows_is_that_of_few(F, dtype):
+    # enough groups that a warp takes more of them; the same bits as a part of the rows alone
+    R, n = 2200, 40
+    g, u, dh = rnd(R, F, sigma=3, dtype=dtype), rnd(R, F, seed=1, dtype=dtype), rnd(R, F, seed=2, dtype=dtype)
+    h, kept = moe.moe_swiglu_save(g, u)
+    dg, du, again = moe.moe_swiglu_backward(dh, kept, rebuild_h=True)
+    for at in (slice(0, n), slice(R - n, R)):
+        h1, kept1 = moe.moe_swiglu_save(g[at], u[at])
+        assert torch.equal(h[at], h1)
+        for a, b in ((kept.g, kept1.g), (kept.u, kept1.u)):
+            assert torch.equal(a.codes[at], b.codes) and torch.equal(a.exps[at], b.exps)
+        for a, b in zip((dg, du, again), moe.moe_swiglu_backward(dh[at], kept1, rebuild_h=True)):
+            assert torch.equal(a[at], b)
+
+
 # ------------------------------------------------------------------ adapters
 def ref_adapters(x, y, A, B, scale, ids):
     """64-bit result and the sum of the magnitudes behind the low-rank term."""
