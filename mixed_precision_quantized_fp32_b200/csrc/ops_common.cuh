@@ -34,52 +34,13 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// N consecutive values <-> fp32 registers.  N = 1 asks for the type's own alignment,
-// any other N for 16 bytes.
-template <typename T, int N>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = to_f32<T>(__ldg(p));
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(w[j]);
-        v[8 * i + 2 * j] = f.x, v[8 * i + 2 * j + 1] = f.y;
-      }
-    }
-  }
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
-  if constexpr (N == 1) {
-    *p = from_f32<T>(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i)
-      reinterpret_cast<uint4*>(p)[i] =
-          make_uint4(pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
-                     pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7]));
-  }
-}
-
-// N consecutive values as they lie in memory, to have many loads on their way before the
-// first is used: 16 bytes (N = 8 of a 16-bit type, 4 of fp32), or one value (N = 1).
-template <typename T, int N> struct Raw { using type = uint4; };
+// N consecutive values as they lie in memory, in one access of 2 to 16 bytes (N = 8 only of a
+// 16-bit type), so that many loads are on their way before the first is used.
+template <int B> struct Access;
+template <> struct Access<4> { using type = uint32_t; };
+template <> struct Access<8> { using type = uint2; };
+template <> struct Access<16> { using type = uint4; };
+template <typename T, int N> struct Raw { using type = typename Access<N * (int)sizeof(T)>::type; };
 template <typename T> struct Raw<T, 1> { using type = T; };
 
 template <typename T, int N>
@@ -87,9 +48,13 @@ __device__ __forceinline__ void decode_raw(const typename Raw<T, N>::type& q, fl
   if constexpr (N == 1) {
     v[0] = to_f32<T>(q);
   } else {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    constexpr int W = N * sizeof(T) / 4;
+    uint32_t w[4] = {};
+    if constexpr (W == 1) w[0] = q;
+    else w[0] = q.x, w[1] = q.y;
+    if constexpr (W == 4) w[2] = q.z, w[3] = q.w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < W; ++j) {
       if constexpr (sizeof(T) == 4) {
         v[j] = __uint_as_float(w[j]);
       } else {
@@ -101,7 +66,33 @@ __device__ __forceinline__ void decode_raw(const typename Raw<T, N>::type& q, fl
 }
 template <typename R> __device__ __forceinline__ R zero_raw() {
   if constexpr (sizeof(R) == 16) return make_uint4(0, 0, 0, 0);
+  else if constexpr (sizeof(R) == 8) return make_uint2(0, 0);
   else return R(0.0f);
+}
+
+// N values rounded and stored, in accesses of up to 16 bytes.
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    *p = from_f32<T>(v[0]);
+  } else {
+    constexpr int W = N * sizeof(T) / 4;
+    uint32_t w[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(v[j]);
+      else w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
+    }
+    if constexpr (W == 1) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (W == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- clusters

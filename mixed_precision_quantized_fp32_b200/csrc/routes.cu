@@ -375,7 +375,7 @@ __device__ __forceinline__ void entries_of(int64_t t, const int32_t* inv, const 
 // in flight (1: 24.2 us, the compiler's own choice 32.5, for 4096 x 8 rows of 2048 bf16);
 // single values want 6 (4096 x 8 rows of 2047: 50 us, with 1 76).
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, N == 1 ? 6 : K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
+__global__ void __launch_bounds__(256, N * sizeof(T) < 16 ? 6 : K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
                                                            const float* __restrict__ w,
                                                            const int32_t* __restrict__ inv, int T_, int k, int cols,
                                                            T* __restrict__ y, int64_t ldy, int shift) {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256, N == 1 ? 6 : K <= 2 ? 8 : K <= 4 ? 4 : 1)
 // 2048 x 2 rows of 4096 bf16: 16.0 us; 18.5 with one piece in flight, 18 to 19 with fewer
 // or more registers a thread.
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, N == 1 ? (K <= 4 ? 6 : 4) : K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
+__global__ void __launch_bounds__(256, N * sizeof(T) < 16 ? (K <= 4 ? 6 : 4) : K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
                                                                const T* __restrict__ o, int64_t ldo,
                                                                const float* __restrict__ w,
                                                                const int32_t* __restrict__ inv, int T_, int k, int cols,
@@ -581,7 +581,7 @@ cudaError_t dispatch_as(const int32_t* idx, int T, int k, int E, int32_t* perm, 
 template <typename T, int N, int K>
 cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y,
                        cudaStream_t stream) {
-  constexpr int U = N == 1 && K <= 2 ? 4 : 2;
+  constexpr int U = N * sizeof(T) < 16 && K <= 2 ? 4 : 2;
   const int cols = H / N, shift = walk_shift(cols, U, 256);
   const unsigned blocks = walk_blocks(T_, 256, shift);
   unsigned ny = 1;  // column blocks: more parallelism for few tokens
@@ -593,7 +593,7 @@ cudaError_t collect_as(ConstRows o, const float* w, const int32_t* inv, int T_, 
 template <typename T, int N, int K>
 cudaError_t collect_backward_as(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
                                 Rows d_o, float* dw, cudaStream_t stream) {
-  constexpr int U = N == 1 && K > 4 ? 4 : 2;
+  constexpr int U = N * sizeof(T) < 16 && K > 4 ? 4 : 2;
   const int cols = H / N;
   const int shift = walk_shift(cols, U, 256);
   return launch_chained(collect_backward_kernel<T, N, K, U>, dim3(walk_blocks(T_, 256, shift)), dim3(256), 0, stream,
@@ -615,7 +615,31 @@ cudaError_t collect_backward_k(ConstRows dy, ConstRows o, const float* w, const 
                   : collect_backward_as<T, N, 8>(dy, o, w, inv, T_, k, H, d_o, dw, s);
 }
 
-bool rows16(const void* p, int64_t ld, int es) { return on16(p) && (ld * es) % 16 == 0; }
+// The most values, a power of two up to 16 bytes, that all these bits (addresses, pitches and
+// widths in bytes) are multiples of.
+int values_at_once(uint64_t bits, int es) {
+  int n = 16 / es;
+  while (bits % (uint64_t)(n * es) != 0) n /= 2;
+  return n;
+}
+
+template <typename T>
+cudaError_t collect_n(int n, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H, Rows y, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (n == 8) return collect_k<T, 8>(o, w, inv, T_, k, H, y, s);
+  return n == 4   ? collect_k<T, 4>(o, w, inv, T_, k, H, y, s)
+         : n == 2 ? collect_k<T, 2>(o, w, inv, T_, k, H, y, s)
+                  : collect_k<T, 1>(o, w, inv, T_, k, H, y, s);
+}
+template <typename T>
+cudaError_t collect_backward_n(int n, ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T_, int k, int H,
+                               Rows d_o, float* dw, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (n == 8) return collect_backward_k<T, 8>(dy, o, w, inv, T_, k, H, d_o, dw, s);
+  return n == 4   ? collect_backward_k<T, 4>(dy, o, w, inv, T_, k, H, d_o, dw, s)
+         : n == 2 ? collect_backward_k<T, 2>(dy, o, w, inv, T_, k, H, d_o, dw, s)
+                  : collect_backward_k<T, 1>(dy, o, w, inv, T_, k, H, d_o, dw, s);
+}
 
 }  // namespace
 
@@ -631,6 +655,7 @@ cudaError_t launch_dispatch(const int32_t* idx, int T, int k, int E, int32_t* pe
   const uint64_t all = (uintptr_t)x.p | (uintptr_t)xs.p | (uint64_t)(x.ld * es) | (uint64_t)(xs.ld * es) |
                        (uint64_t)((int64_t)H * es);
   if ((all & 15) == 0) return dispatch_as<uint4>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
+  if ((all & 7) == 0) return dispatch_as<uint2>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
   if ((all & 3) == 0) return dispatch_as<uint32_t>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
   return dispatch_as<uint16_t>(idx, T, k, E, perm, inv, offsets, x, xs, es, H, ws, stream);
 }
@@ -638,29 +663,21 @@ cudaError_t launch_dispatch(const int32_t* idx, int T, int k, int E, int32_t* pe
 cudaError_t launch_collect(ConstRows o, const float* w, const int32_t* inv, int T, int k, int H, int dtype, Rows y,
                            cudaStream_t stream) {
   const int es = dtype_size(dtype);
-  const bool vec = rows16(o.p, o.ld, es) && rows16(y.p, y.ld, es) && ((int64_t)H * es) % 16 == 0;
-  if (dtype == MOE_F32)
-    return vec ? collect_k<float, 4>(o, w, inv, T, k, H, y, stream) : collect_k<float, 1>(o, w, inv, T, k, H, y, stream);
-  if (dtype == MOE_F16)
-    return vec ? collect_k<__half, 8>(o, w, inv, T, k, H, y, stream)
-               : collect_k<__half, 1>(o, w, inv, T, k, H, y, stream);
-  return vec ? collect_k<__nv_bfloat16, 8>(o, w, inv, T, k, H, y, stream)
-             : collect_k<__nv_bfloat16, 1>(o, w, inv, T, k, H, y, stream);
+  const int n = values_at_once((uintptr_t)o.p | (uintptr_t)y.p | (uint64_t)(o.ld * es) | (uint64_t)(y.ld * es) |
+                                   (uint64_t)((int64_t)H * es), es);
+  if (dtype == MOE_F32) return collect_n<float>(n, o, w, inv, T, k, H, y, stream);
+  return dtype == MOE_F16 ? collect_n<__half>(n, o, w, inv, T, k, H, y, stream)
+                          : collect_n<__nv_bfloat16>(n, o, w, inv, T, k, H, y, stream);
 }
 
 cudaError_t launch_collect_backward(ConstRows dy, ConstRows o, const float* w, const int32_t* inv, int T, int k, int H,
                                     int dtype, Rows d_o, float* dw, cudaStream_t stream) {
   const int es = dtype_size(dtype);
-  const bool vec = rows16(dy.p, dy.ld, es) && rows16(o.p, o.ld, es) && rows16(d_o.p, d_o.ld, es) &&
-                   ((int64_t)H * es) % 16 == 0;
-  if (dtype == MOE_F32)
-    return vec ? collect_backward_k<float, 4>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-               : collect_backward_k<float, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
-  if (dtype == MOE_F16)
-    return vec ? collect_backward_k<__half, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-               : collect_backward_k<__half, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
-  return vec ? collect_backward_k<__nv_bfloat16, 8>(dy, o, w, inv, T, k, H, d_o, dw, stream)
-             : collect_backward_k<__nv_bfloat16, 1>(dy, o, w, inv, T, k, H, d_o, dw, stream);
+  const int n = values_at_once((uintptr_t)dy.p | (uintptr_t)o.p | (uintptr_t)d_o.p | (uint64_t)(dy.ld * es) |
+                                   (uint64_t)(o.ld * es) | (uint64_t)(d_o.ld * es) | (uint64_t)((int64_t)H * es), es);
+  if (dtype == MOE_F32) return collect_backward_n<float>(n, dy, o, w, inv, T, k, H, d_o, dw, stream);
+  return dtype == MOE_F16 ? collect_backward_n<__half>(n, dy, o, w, inv, T, k, H, d_o, dw, stream)
+                          : collect_backward_n<__nv_bfloat16>(n, dy, o, w, inv, T, k, H, d_o, dw, stream);
 }
 
 }  // namespace moe
