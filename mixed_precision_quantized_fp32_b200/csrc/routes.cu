@@ -19,7 +19,8 @@
 //   collect, 8192 x 2, 4096 bf16 (201 MB)                 31.3 us, 99%
 //   its gradient, 2048 x 2, 4096 bf16 (81 MB)             16.0 us, 78%
 //   dispatch of 16 x 6 entries 2.8 us, collect of 64 x 2 rows of 12288 fp32 2.9 us
-// Rows of an odd number of 16-bit values go value by value, at 40 to 50%.
+// Rows whose width, pitch or start is no multiple of 16 bytes go in accesses of 8, 4 or 2 (collect
+// of 8192 x 2 rows of 4092, 4094 and 4095 bf16: 34, 36 and 59 us).
 #include "ops_common.cuh"
 
 namespace moe {
@@ -370,15 +371,20 @@ __device__ __forceinline__ void entries_of(int64_t t, const int32_t* inv, const 
 }
 
 // Sum of a token's expert rows, weighted or not.  U pieces of J rows are on their way
-// before the first sum.  Blocks an SM, by measurement: K = 2 wants many light threads (8:
-// 31.3 us, 6: 33.8, 5: 36.2 for 8192 x 2 rows of 4096 bf16), K = 8 few with all their loads
-// in flight (1: 24.2 us, the compiler's own choice 32.5, for 4096 x 8 rows of 2048 bf16);
-// single values want 6 (4096 x 8 rows of 2047: 50 us, with 1 76).
+// before the first sum.  Blocks an SM by measurement, each the best of three or four budgets:
+// with 16-byte accesses K = 2 wants many light threads (8: 31.3 us, 6: 33.8, 5: 36.2 for 8192 x 2
+// rows of 4096 bf16), K = 8 few with all their loads in flight (1: 24.2 us, the compiler's own
+// choice 32.5, for 4096 x 8 rows of 2048 bf16); smaller accesses want more threads (rows of 2046
+// and 2047: 30.9 and 47.6 us with 6, 40.1 and 67.5 with 8).
+constexpr int collect_blocks(int bytes, int K) {  // bytes: of an access
+  if (bytes == 16) return K <= 2 ? 8 : K <= 4 ? 4 : 1;
+  return bytes == 8 ? (K <= 4 ? 6 : 3) : bytes == 4 && K <= 4 ? 8 : 6;
+}
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, N * sizeof(T) < 16 ? 6 : K <= 2 ? 8 : K <= 4 ? 4 : 1) collect_rows_kernel(const T* __restrict__ o, int64_t ldo,
-                                                           const float* __restrict__ w,
-                                                           const int32_t* __restrict__ inv, int T_, int k, int cols,
-                                                           T* __restrict__ y, int64_t ldy, int shift) {
+__global__ void __launch_bounds__(256, collect_blocks(N * sizeof(T), K))
+    collect_rows_kernel(const T* __restrict__ o, int64_t ldo, const float* __restrict__ w,
+                        const int32_t* __restrict__ inv, int T_, int k, int cols, T* __restrict__ y, int64_t ldy,
+                        int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   using R = typename Raw<T, N>::type;
   constexpr int J = K < 4 ? K : 4;
@@ -427,14 +433,17 @@ __global__ void __launch_bounds__(256, N * sizeof(T) < 16 ? 6 : K <= 2 ? 8 : K <
 // Gradient of collect: dy's row is read once, scaled into each expert row, and its dot
 // product with each expert's output summed over the token's threads in a fixed order.
 // 2048 x 2 rows of 4096 bf16: 16.0 us; 18.5 with one piece in flight, 18 to 19 with fewer
-// or more registers a thread.
+// or more registers a thread.  Blocks an SM by measurement, as above (4096 x 8 rows of 2046
+// fp16: 77.8 us with 3, 84.2 with 4, 124 with 5; 4096 x 2 of 2047 bf16: 28.7 with 8, 32.0 with 6).
+constexpr int gradient_blocks(int bytes, int K) {
+  if (bytes == 16) return K <= 2 ? 5 : K <= 4 ? 4 : 3;
+  return K <= 4 ? (bytes == 8 ? 6 : 8) : bytes == 2 ? 4 : 3;
+}
 template <typename T, int N, int K, int U>
-__global__ void __launch_bounds__(256, N * sizeof(T) < 16 ? (K <= 4 ? 6 : 4) : K <= 2 ? 5 : K <= 4 ? 4 : 3) collect_backward_kernel(const T* __restrict__ dy, int64_t lddy,
-                                                               const T* __restrict__ o, int64_t ldo,
-                                                               const float* __restrict__ w,
-                                                               const int32_t* __restrict__ inv, int T_, int k, int cols,
-                                                               T* __restrict__ d_o, int64_t lddo,
-                                                               float* __restrict__ dw, int shift) {
+__global__ void __launch_bounds__(256, gradient_blocks(N * sizeof(T), K))
+    collect_backward_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ o, int64_t ldo,
+                            const float* __restrict__ w, const int32_t* __restrict__ inv, int T_, int k, int cols,
+                            T* __restrict__ d_o, int64_t lddo, float* __restrict__ dw, int shift) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   using R = typename Raw<T, N>::type;
   constexpr int J = K < 8 ? 2 : 4;

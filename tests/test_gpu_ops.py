@@ -167,6 +167,37 @@ def test_collect_and_gradients(T, k, E, H, kind, dtype):
     assert bool((dw[~real] == 0).all())
 
 
+# rows in accesses of 8, 4 and 2 bytes
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("k", [1, 2, 3, 8])
+@pytest.mark.parametrize("H", [2, 12, 258, 1020, 1022, 1023])
+def test_rows_in_fours_pairs_and_singles(H, k, dtype):
+    test_collect_and_gradients(70, k, 9, H, "holes", dtype)
+    test_dispatch(70, k, 9, H, "holes", dtype)
+
+
+@pytest.mark.parametrize("H,pitch,offset", [(256, 260, 4), (256, 258, 2), (260, 264, 0), (258, 264, 6)])
+def test_collect_through_views(H, pitch, offset):
+    T, k, E = 90, 3, 7
+    idx, o, dy, w = index(T, k, E, "holes"), rnd(T * k, H, dtype=F16), rnd(T, H, dtype=F16, seed=1), rnd(T, k, seed=2)
+    r = moe.moe_sort(idx, E)
+    total = int(r.offsets[E])
+    ov, dyv = spaced(o, pitch, offset)[0], spaced(dy, pitch, offset)[0]
+    y, mem = spaced(torch.zeros(T, H, dtype=F16, device="cuda"), pitch, offset)
+    do, dmem = spaced(torch.zeros(T * k, H, dtype=F16, device="cuda"), pitch, offset)
+    moe.moe_collect(ov, w, r, y=y)
+    _, dw = moe.moe_collect_backward(dyv, ov, w, r, do=do)
+    assert torch.equal(y, moe.moe_collect(o, w, r))
+    do1, dw1 = moe.moe_collect_backward(dy, o, w, r)
+    assert torch.equal(do[:total], do1[:total])
+    # dw: H products, in another order
+    dot = (dy.to(F64)[:, None] * torch.where((r.inv >= 0).reshape(T, k, 1), o.to(F64)[r.inv.clamp(min=0).long()].reshape(T, k, H), 0.0))
+    assert bool(((dw - dw1).abs().to(F64) <= 2 * (H + 2) * U * dot.abs().sum(2)).all())
+    for m in (mem, dmem):
+        m[:, offset:offset + H] = 7.0
+        assert bool((m == 7.0).all())
+
+
 def tiny(dtype):
     """Half the smallest step of a type: the rounding of results below its normal range."""
     return torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
