@@ -708,19 +708,14 @@ struct Shares {
   int tiles, cluster, kslice, nslice;
 };
 // tiles: an upper bound on the tiles of TM rows; half of the last tiles of the adapters are
-// expected.  A tile gets blocks, each with at least a step of k or of outputs, while all fit
-// the machine at once (per_sm: blocks an SM holds): 64-token tiles of 8192 tokens of 24
-// adapters, r 64, take 31.2 us with 2 blocks a tile and 37.6 with 1; of 32 adapters, r 128, one
-// block an SM, 42.8 with 1 and 49.7 with 2; 2048 tokens of 16, r 64, 29.0 with 4 and 33.6 with 8,
-// more than fit.  16-token tiles get more where a block would read over `much` bytes of its
-// adapter: 1 MB over 4 blocks took 16.4 us, over 8 12.5.
-Shares shares_of(const AdapterArgs& a, int TM, int kstep, int per_sm, int64_t much) {
+// expected.  A tile gets blocks, each with at least a step of k or of outputs, while the
+// kernel's rule has room for all of them.
+template <typename Fits>
+Shares shares_of(const AdapterArgs& a, int TM, int kstep, Fits fits) {
   const int most = a.T < a.n ? a.T : a.n, full = a.T / TM, likely = full + (most + 1) / 2;
   Shares s{most + full, 1, 0, 0};
-  auto more = [&] {
-    return 2 * likely * s.cluster <= 148 * per_sm || (int64_t)a.r * (a.K + a.N) * 2 / s.cluster > much;
-  };
-  while (s.cluster < kAdMaxCluster && std::max(a.K, a.N) > s.cluster * kstep && more()) s.cluster *= 2;
+  while (s.cluster < kAdMaxCluster && std::max(a.K, a.N) > s.cluster * kstep && fits(2 * likely * s.cluster, s.cluster))
+    s.cluster *= 2;
   s.kslice = ((a.K + s.cluster - 1) / s.cluster + 31) / 32 * 32;
   s.nslice = ((a.N + s.cluster - 1) / s.cluster + 31) / 32 * 32;
   return s;
@@ -731,10 +726,22 @@ cudaError_t allow_smem(Kern kern, int smem) {
   return smem > 48 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
 }
 
+// 16-token tiles: a block an SM, since two share the path from L2 that the adapters take (300
+// tokens of 2 adapters, K = N = 2048, r 128, 4 blocks a tile 11.7 us, 8 14.2; 600 of 8, 4096 ->
+// 1000, r 64, 2 blocks 11.3, 8 15.9; 100 of 60, 2048, r 32, 4 blocks 7.2, 8 8.4).  Two an SM, and a
+// tenth more since some tokens have no adapter, at ranks up to 16, where latency counts for more
+// (K = N = 4096, r 16: 1024 tokens of 32 adapters 17.8 us with 2 blocks a tile, 11.8 with 4; 64 of 48
+// 7.8 with 4, 6.3 with 8), and where each tile brings much of an adapter of its own from memory
+// (64 of 48, r 64: 14.9 with 4, 10.9 with 8).
 template <typename T, int NR>
 cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
   constexpr int KB = (NR + 3) / 4, smem = ((kAdWarps + 1) * 16 * NR * 8 + 16 * (KB * 32 + 4)) * (int)sizeof(float);
-  const Shares p = shares_of(a, 16, kAdWarps * 32, NR <= 8 ? 2 : 1, 96 * 1024);
+  const bool own = a.T <= 16 * a.n;
+  const Shares p = shares_of(a, 16, kAdWarps * 32, [&](int blocks, int cluster) {
+    if (blocks <= 148) return true;
+    const bool much = own && (int64_t)a.r * (a.K + a.N) * 2 / cluster > 96 * 1024;
+    return NR <= 8 && (NR <= 2 || much) && blocks <= 2 * 148 * 11 / 10;
+  });
   const cudaError_t e = allow_smem(adapter_kernel<T, NR>, smem);
   if (e != cudaSuccess) return e;
   return launch_cluster(adapter_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kAdThreads), p.cluster, smem, s,
@@ -742,9 +749,12 @@ cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
                         (const T*)a.B, a.scale, a.perm, a.offsets, a.out.p != a.y.p, p.cluster, p.kslice, p.nslice,
                         (T*)a.out.p, a.out.ld);
 }
+// 64-token tiles: as many as an SM holds.  8192 tokens of 24 adapters, r 64, take 31.2 us with 2
+// blocks a tile and 37.6 with 1; of 32 adapters, r 128, one block an SM, 42.8 with 1 and 49.7 with 2;
+// 2048 tokens of 16, K = N = 4096, r 64, 29.0 with 4 and 33.6 with 8, more than fit.
 template <typename T, int NR>
 cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
-  const Shares p = shares_of(a, kWideTokens, 64, NR <= 8 ? 2 : 1, INT64_MAX);
+  const Shares p = shares_of(a, kWideTokens, 64, [](int blocks, int) { return blocks <= 148 * (NR <= 8 ? 2 : 1); });
   const cudaError_t e = allow_smem(adapter_wide_kernel<T, NR>, wide_smem_bytes<NR>());
   if (e != cudaSuccess) return e;
   return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kWideThreads), p.cluster,
@@ -754,14 +764,19 @@ cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
 }
 
 // Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of
-// many adapters) and for short batches of low rank; tiles of 64 where adapters have rows
-// enough to fill them.  K = N = 4096, 16- against 64-token tiles: 128 tokens 5.6 / 11.4 us
-// (r 16), 8.7 / 14.4 (r 64); 1024 tokens of r 16 11.9 / 16.4; 256 of r 64 11.8 / 14.4; 512 of
-// r 128 (K = N = 2048) 26.3 / 16.0; 2048 of r 64 49.9 / 33.8; 512 tokens over 64 adapters
-// 10.5 / 22.5.
+// many adapters) and where there is little to multiply; tiles of 64 where adapters have rows
+// enough to fill them.  16- against 64-token tiles (T, K, N, r, adapters):
+//   350, 2896, 2896, 96, 1    13.8 / 16.8 us       2048, 1024, 1024, 64, 16   11.7 / 10.4
+//   512, 2048, 2048, 128, 4   11.9 / 16.3          2048, 2048, 2048, 32, 16   17.4 / 13.6
+//   1024, 2048, 2048, 64, 8   11.8 / 14.3          1000, 4096, 4096, 32, 8    17.0 / 15.4
+//   1024, 4096, 4096, 16, 32  12.4 / 16.7          8192, 256, 256, 64, 24     15.7 / 10.6
+//   2048, 1024, 1024, 32, 16   8.3 /  9.4          2048, 4096, 4096, 64, 16   43.9 / 24.5
+//   512, 4096, 4096, 16, 64   10.5 / 22.5          8192, 128, 128, 8, 24       9.8 / 8.1
 template <typename T>
 cudaError_t adapters_of(const AdapterArgs& a, cudaStream_t s) {
-  if (a.T <= 128 || a.T < 16 * a.n || a.T * a.r <= 16384) {
+  const int64_t products = (int64_t)a.T * a.r * (a.K + a.N);
+  if (a.T <= 128 || a.T < 16 * a.n || (a.T <= 1024 && products <= 275000000) ||
+      (a.T <= 2048 && products <= 150000000)) {
     if (a.r <= 16) return adapters_short<T, 2>(a, s);
     if (a.r <= 32) return adapters_short<T, 4>(a, s);
     return a.r <= 64 ? adapters_short<T, 8>(a, s) : adapters_short<T, 16>(a, s);

@@ -525,7 +525,7 @@ def test_adapters_all_or_none(kind, T, r):
         assert torch.equal(out, y)
 
 
-@pytest.mark.parametrize("T,r", [(150, 32), (600, 64)])   # tiles of 16 and of 64 tokens
+@pytest.mark.parametrize("T,r", [(150, 32), (600, 64)])
 def test_adapters_through_views(T, r):
     K, N, n = 264, 520, 5
     ids = index(T, 1, n, "holes")[:, 0]
@@ -556,7 +556,7 @@ def test_adapters_beyond_half_range(T):
     assert adapters_near(moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, n)), want, mag, K, r, F16)
 
 
-@pytest.mark.parametrize("T,r", [(20, 8), (300, 128)])   # tiles of 16 and of 64 tokens
+@pytest.mark.parametrize("T,r", [(20, 8), (300, 128), (2100, 32)])   # tiles of 16 and of 64 tokens
 def test_adapters_infinite_beside_large(T, r):
     # a low-rank term beyond 32 bits next to one of 2^79, of the other sign: infinite as the
     # formula's sum is, not the difference of two infinities
@@ -586,6 +586,60 @@ def test_adapters_keep_requests_apart(T, r):
     rest = [t for t in range(T) if t not in (7, 20)]
     assert torch.equal(out[rest], clean[rest])
     assert bool(torch.isnan(out[7]).all()) and not bool(torch.isfinite(out[20]).any())
+
+
+# tiles of 64 tokens: long batches, and shorter ones with more to multiply (up to eight blocks a tile)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,K,N,r,n", [
+    (2049, 8, 8, 8, 1), (2100, 264, 40, 16, 3), (2060, 40, 1000, 24, 2), (2500, 320, 264, 64, 7), (2400, 264, 288, 128, 3),
+    (3000, 512, 512, 40, 100), (2200, 2056, 328, 40, 2), (2300, 72, 2000, 120, 6), (1100, 2056, 1096, 64, 2), (1030, 136, 1000, 128, 4),
+    (900, 2056, 3000, 72, 1), (400, 4104, 2000, 120, 1), (2048, 1552, 2000, 32, 5)])
+def test_adapters_in_large_tiles(T, K, N, r, n, dtype):
+    test_adapters(T, K, N, r, n, dtype)
+
+
+@pytest.mark.parametrize("r", [16, 64, 128])
+def test_adapters_in_large_tiles_as_programs_call_them(r):
+    T = 2150
+    for kind in ("none", "one"):
+        test_adapters_all_or_none(kind, T, r)
+    test_adapters_through_views(T, r)
+    test_adapters_keep_requests_apart(T, r)
+    test_adapters_beyond_half_range(T)
+
+
+def test_large_tiles_on_streams_and_in_graphs():
+    # two captured graphs, replayed in turn with new inputs, beside a call on another stream
+    T, H, n = 2300, 264, 9
+    x, y, ids = rnd(T, H, dtype=BF16), rnd(T, H, dtype=BF16, seed=1), index(T, 1, n, "holes")[:, 0]
+    banks = [bank(n, r, H, H, BF16) for r in (64, 128)]
+
+    def step(stream=None):
+        routes = moe.moe_sort(ids, n, stream=stream)
+        return [moe.moe_adapters(x, y, *b, routes, stream=stream) for b in banks]
+
+    want = step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    s = torch.cuda.Stream()
+    for seed in (3, 4):
+        x.copy_(rnd(T, H, dtype=BF16, seed=seed))
+        ids.copy_(index(T, 1, n, "holes", seed=seed)[:, 0])
+        torch.cuda.synchronize()
+        other = step(stream=s)
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        now = step()
+        for (_, out), extra in zip(graphs, (other, now)):
+            for a, b, c in zip(out, extra, now):
+                assert torch.equal(a, c) and torch.equal(b, c)
+        assert not torch.equal(now[0], want[0])
 
 
 # ------------------------------------------------------------------ offsets beyond 32 bits
