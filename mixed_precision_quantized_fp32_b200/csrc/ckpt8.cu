@@ -21,8 +21,8 @@
 // run with fewer values a lane.  Of the measured copy rate:
 //   save and load, 8192 x 4096 bf16 (203 MB)               31.2 us, 101%
 //   SwiGLU forward and backward, 4096 x 14336 bf16 (1.06 GB)  162 us, 102%
-//   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 46, 50, 68 us
-//   (69, 63, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 81, 114 us (81, 71, 50%)
+//   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 47, 49, 68 us
+//   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 81, 114 us (81, 71, 50%)
 #include <initializer_list>
 
 #include "ops_common.cuh"
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(
 // Any width, pitch and alignment: a lane has N consecutive values in accesses of V (4, 2 or 1,
 // what widths, rows and codes are aligned to; N >= V).  A warp takes N groups of a row at once,
 // S times, with all loads in flight, and finds the row once.  The number of instructions bounds
-// these kernels, so what a group needs once is shared by few lanes, as far as the accesses then
-// leave the bytes between them to the next: single values, save and load of 8192 x 4095 bf16,
-// take 68 us with N = 2 (1: 76, 4: 71); the SwiGLU kernels, with more to do for a value, 114 for
-// 4096 x 5001 with N = 1 (4: 135).  Pairs take N = 4: 50 us where N = 2 took 58.
+// these kernels, and few lanes a group save what each of them computes for it; but a larger N
+// spreads an access over more lines.  Single values: save and load of 8192 x 4095 bf16 take 68 us
+// with N = 2 (1: 76, 4: 71); the SwiGLU kernels, with more to do for a value, 114 for 4096 x 5001
+// with N = 1 (4: 135).  Pairs take N = 4: save and load of 8192 x 4094 49 us, with N = 2 58.
 template <int V> constexpr int kMany = V == 1 ? 2 : 4;  // N of save and load
 template <int V> constexpr int kSpan = 8 / kMany<V>;    // their S
 template <int V> constexpr int kFew = V == 1 ? 1 : 4;   // N of the SwiGLU kernels
