@@ -12,9 +12,12 @@
 // launches with partial sums in a workspace took 9.6 us for 64 requests where this takes
 // 6.6, and 104 us for the long batch below.)
 //
-// The up product's fp32 operand P goes in as two terms of the value type (P = hi + lo, 16 or
-// more bits), so its rounding stays far below that of the stored result; in fp16 a row is
-// first brought to at most 2^14 by a power of two, since P may pass fp16's range.
+// The up product's fp32 operand P goes in as two terms of the value type, P = hi + lo: to within
+// 2^-17 of a value in bf16 and 2^-23 in fp16, so its rounding stays far below that of the stored
+// result.  In fp16 a row's largest magnitude is first brought to 2^13 .. 2^14 by a power of two,
+// since P may pass fp16's range at either end: unscaled, lo would be subnormal for values below
+// 2^-3, and terms near 2^-20 keep 5 bits.  Values far below their row's largest are off by at
+// most 2^-38 of that.
 //
 // Two kernels.  Decode batches: tiles of 16 tokens on mma.sync, operands from memory straight
 // to fragments (the contraction index may be permuted if both operands are permuted alike,
@@ -150,10 +153,17 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
-// The power of two that brings a row of P, whose largest magnitude has these bits, into
-// [2^13, 2^14).  An infinity is taken for the largest finite value: it stays infinite, and the
-// finite terms beside it stay finite.
-__device__ __forceinline__ int exponent_beyond(uint32_t big) { return (int)(min(big, 0x7F7FFFFFu) >> 23) - 127 - 13; }
+// The power of two 2^-e that brings a row of P, whose largest magnitude has these bits, into
+// [2^13, 2^14), and 2^e, which takes it back.  An infinity is taken for the largest finite value: it
+// stays infinite, and the finite terms beside it stay finite.  Rows below 2^-87 go up by 2^100 only,
+// so that both powers are ordinary numbers: no B makes such a row more than 2^-63.
+struct RowScale {
+  float down, back;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t big) {
+  const int e = max((int)(min(big, 0x7F7FFFFFu) >> 23) - 127 - 13, -100);
+  return {__uint_as_float((uint32_t)(127 - e) << 23), __uint_as_float((uint32_t)(127 + e) << 23)};
+}
 
 // Eight values of a lane, its share of 32 of the rank, as the MMA's first operand (h: row g or
 // g + 8): pairs 0, 1 to the first MMA, 2, 3 to the second, as B's.
@@ -216,15 +226,12 @@ __device__ __forceinline__ void operand_p(const float* P, uint32_t (&hi)[KB][2][
         for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(p[b][i]) & 0x7FFFFFFFu);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int e = exponent_beyond(big);
-      if (e > 0) {
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        back[h] = __uint_as_float((uint32_t)(127 + e) << 23);
+      const RowScale by = row_scale(big);
+      back[h] = by.back;
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+      for (int b = 0; b < KB; ++b)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) p[b][i] *= down;
-      }
+        for (int i = 0; i < 8; ++i) p[b][i] *= by.down;
     }
 #pragma unroll
     for (int b = 0; b < KB; ++b) split8<T>(p[b], h, hi[b], lo[b]);
@@ -624,11 +631,9 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
                            max(__float_as_uint(s.z) & 0x7FFFFFFFu, __float_as_uint(s.w) & 0x7FFFFFFFu));
 #pragma unroll
         for (int o = PIECES / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-        const int e = exponent_beyond(big);
-        const bool scaled = e > 0;
-        const float by = scaled ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
-        s.x *= by, s.y *= by, s.z *= by, s.w *= by;
-        if (piece == 0) undo[row] = scaled ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.0f;
+        const RowScale by = row_scale(big);
+        s.x *= by.down, s.y *= by.down, s.z *= by.down, s.w *= by.down;
+        if (piece == 0) undo[row] = by.back;
       }
       uint32_t hi[2], lo[2];
       split2<T>(s.x, s.y, hi[0], lo[0]);
