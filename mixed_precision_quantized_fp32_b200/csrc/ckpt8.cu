@@ -24,6 +24,7 @@
 //   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 47, 49, 68 us
 //   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 81, 114 us (81, 71, 50%)
 #include <initializer_list>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -152,17 +153,126 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t eb, float (&v)[8]) {
   decode<8>(q, eb, v);
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Arithmetic on one value or on two, which share an instruction (f32x2).  The kernels with eight values a
+// lane take pairs: what they have to compute for a value takes as long as its bytes (backward of
+// 4096 x 14336 bf16 92 us, with single values 96).
+__device__ __forceinline__ uint64_t join(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float mul_add(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(join(a)), "l"(join(b)));
+  return split(r);
+}
+__device__ __forceinline__ float2 mul(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(join(a)), "l"(join(b)));
+  return split(r);
+}
+__device__ __forceinline__ float2 mul_add(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(join(a)), "l"(join(b)), "l"(join(c)));
+  return split(r);
+}
+template <typename F> __device__ __forceinline__ F all(float v);
+template <> __device__ __forceinline__ float all<float>(float v) { return v; }
+template <> __device__ __forceinline__ float2 all<float2>(float v) { return make_float2(v, v); }
+template <float (*Op)(float)> __device__ __forceinline__ float each(float a) { return Op(a); }
+template <float (*Op)(float)> __device__ __forceinline__ float2 each(float2 a) { return make_float2(Op(a.x), Op(a.y)); }
+template <float (*Op)(float, float)> __device__ __forceinline__ float each(float a, float b) { return Op(a, b); }
+template <float (*Op)(float, float)> __device__ __forceinline__ float2 each(float2 a, float2 b) {
+  return make_float2(Op(a.x, b.x), Op(a.y, b.y));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // to 2^-22 of the value
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {  // to a unit of the last place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+__device__ __forceinline__ float not_below_110(float x) { return fmaxf(x, -110.0f); }
+// The larger magnitude with the sign of a * b (NaN if either is one), and the smaller.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(fabsf(a), fabsf(b)); }
+
+// s = 1/(1+exp(-g)) and 1 - s.  With v = 2^-32 exp(-g), which stays below 2^127 (from -110 on s is zero),
+//   2^32 s = 1/(2^-32 + v)   and   1 - s = v * 2^32 s:
+// nothing overflows, s keeps its bits down to fp32's least numbers (1/(1+exp(-g)) would be zero from
+// -88 on), and 1 - s loses none to a subtraction.  fp32 values: s to 12 * 2^-24 of it, by the library's
+// exponential (its square, since of -g it would overflow).  16-bit values: to (31 + 1.3 |g|) 2^-24, as v is a
+// power of two of one rounded product; 2^-16.5 at -104, far below their own steps.
+template <typename F> struct Sigmoid {
+  F s, rest;
+};
+template <typename T, typename F>
+__device__ __forceinline__ Sigmoid<F> sigmoid(F g) {
+  const F b = each<not_below_110>(g);
+  F v;
+  if constexpr (sizeof(T) == 4) {
+    const F root = mul(each<exp_of>(mul(b, all<F>(-0.5f))), all<F>(0x1p-16f));
+    v = mul(root, root);
+  } else {
+    v = each<exp2_fast>(mul_add(b, all<F>(-1.44269504f), all<F>(-32.0f)));  // 1/ln 2
+  }
+  const F s32 = each<reciprocal>(add(v, all<F>(0x1p-32f)));
+  return {mul(s32, all<F>(0x1p-32f)), mul(v, s32)};
+}
 
 // silu(g) * u.  At g = -inf this is -inf * 0: NaN, as the formula says.
-__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
+template <typename T, typename F>
+__device__ __forceinline__ F swiglu(F g, F u) {
+  return mul(mul(g, sigmoid<T>(g).s), u);
+}
 
-struct Grads {
-  float dg, du, h;
-};
-__device__ __forceinline__ Grads swiglu_grad(float g, float u, float dh) {
-  const float s = sigmoid(g), a = g * s;
-  return {dh * u * (s * fmaf(g, 1.0f - s, 1.0f)), dh * a, a * u};
+// From g, u and dh: du in g, h in u and dg in dh.  dg = d * dh * u with d = s (1 + g (1 - s)), at most 1.1: dh * u
+// may pass fp32's range where the whole does not, and d times the smaller of the two may fall below it, so
+// d takes the larger one first.  (In fp16 neither can happen.)
+template <typename T, typename F>
+__device__ __forceinline__ void swiglu_grad(F& g, F& u, F& dh) {
+  const Sigmoid<F> y = sigmoid<T>(g);
+  const F a = mul(g, y.s), d = mul(y.s, mul_add(g, y.rest, all<F>(1.0f)));
+  F dg;
+  if constexpr (std::is_same<T, __half>::value) dg = mul(mul(d, dh), u);
+  else dg = mul(mul(d, each<larger>(dh, u)), each<smaller>(dh, u));
+  g = mul(dh, a), u = mul(a, u), dh = dg;
+}
+
+// Eight values, in pairs.
+template <typename T>
+__device__ __forceinline__ void swiglu8(float (&g)[8], const float (&u)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 h = swiglu<T>(make_float2(g[i], g[i + 1]), make_float2(u[i], u[i + 1]));
+    g[i] = h.x, g[i + 1] = h.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void swiglu_grad8(float (&g)[8], float (&u)[8], float (&dh)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    float2 a = make_float2(g[i], g[i + 1]), b = make_float2(u[i], u[i + 1]), d = make_float2(dh[i], dh[i + 1]);
+    swiglu_grad<T>(a, b, d);
+    g[i] = a.x, g[i + 1] = a.y, u[i] = b.x, u[i + 1] = b.y, dh[i] = d.x, dh[i + 1] = d.y;
+  }
 }
 
 // Where a lane works: group `at` of the rows in order, value `col` of row `row`.
@@ -286,14 +396,14 @@ __global__ void __launch_bounds__(256) swiglu_save_kernel(const T* __restrict__ 
       ge[ge_at] = (uint8_t)ea;
       ue[ge_at] = (uint8_t)eb;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = swiglu(a[j], b[j]);
+    swiglu8<T>(a, b);
     store_vec<T, 8>(h + p[i].row * ldh + p[i].col, a);
   }
 }
 
+// Five blocks an SM for 16-bit values (48 registers; without the bound 58, and 101 us for 92).
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(256) swiglu_backward_kernel(
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) swiglu_backward_kernel(
     const T* __restrict__ dh, int64_t lddh, const int8_t* __restrict__ gq, const uint8_t* __restrict__ ge,
     const int8_t* __restrict__ uq, const uint8_t* __restrict__ ue, int R, int F, T* __restrict__ dg, int64_t lddg,
     T* __restrict__ du, int64_t lddu, T* __restrict__ h, int64_t ldh, const int32_t* __restrict__ n_rows) {
@@ -321,11 +431,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(
     values8(e[i], d);
     decode8(cg[i], eg[i], a);
     decode8(cu[i], eu[i], b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const Grads r = swiglu_grad(a[j], b[j], d[j]);
-      d[j] = r.dg, a[j] = r.du, b[j] = r.h;
-    }
+    swiglu_grad8<T>(a, b, d);
     store_vec<T, 8>(dg + p[i].row * lddg + p[i].col, d);
     store_vec<T, 8>(du + p[i].row * lddu + p[i].col, a);
     if (h) store_vec<T, 8>(h + p[i].row * ldh + p[i].col, b);
@@ -512,7 +618,7 @@ __global__ void __launch_bounds__(256) swiglu_save_v_kernel(const T* __restrict_
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) a[i][j] = swiglu(a[i][j], b[i][j]);
+    for (int j = 0; j < N; ++j) a[i][j] = swiglu<T>(a[i][j], b[i][j]);
   store_span<V>(h + s.row * ldh + s.col, s.left, a);
 }
 
@@ -537,10 +643,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_v_kernel(
     decode<N>(cg[i], eg[i], a[i]);
     decode<N>(cu[i], eu[i], b[i]);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const Grads r = swiglu_grad(a[i][j], b[i][j], d[i][j]);
-      d[i][j] = r.dg, a[i][j] = r.du, b[i][j] = r.h;
-    }
+    for (int j = 0; j < N; ++j) swiglu_grad<T>(a[i][j], b[i][j], d[i][j]);
   }
   store_span<V>(dg + s.row * lddg + s.col, s.left, d);
   store_span<V>(du + s.row * lddu + s.col, s.left, a);

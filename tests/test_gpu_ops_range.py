@@ -10,7 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import mixed_precision_quantized_fp32_b200 as moe  # noqa: E402
-from tests.test_gpu_ops import F16, F64, bank, half_step, index, ref_adapters, rnd  # noqa: E402
+from tests.test_gpu_ops import BF16, F16, F32, F64, U, bank, half_step, index, ref_adapters, rnd  # noqa: E402
 
 
 # ------------------------------------------------------------------ adapters: small low-rank terms
@@ -43,3 +43,61 @@ def test_adapters_of_small_terms_in_fp16(T, r, small):
     assert not bool(out[3].any())
     if small < 100:                              # ordinary numbers, so that half a step is what counts
         assert float(want.abs().median()) > 2.0 ** -12
+
+
+# ------------------------------------------------------------------ SwiGLU: far gates, large factors
+def swiglu_errors(g, u, dh, dtype):
+    """Bounds on the fp32 errors of h, du and dg, in 64 bits.  The kernels take v = 2^-32 exp(-g), 2^32 s = 1/(2^-32 + v)
+    and 1 - s = v * 2^32 s.  v is off by
+      fp32: twice 2 units in the last place of exp(-g/2), 8 U, and U for the square: 9 U;
+      16-bit: the exponent 32 + 1.443 |g| is rounded once and its factor once before, (32 + 1.8 |g|) U ln 2, and
+        the power is off by 2^-22: (27 + 1.3 |g|) U.
+    The sum adds U and the reciprocal, one unit in the last place, 2 U to s; its product another U to 1 - s.  s
+    is held in steps of 2^-149 where it is subnormal.  Products and sums behind it add U each."""
+    v = 9.0 if dtype is F32 else 27 + 1.3 * g.abs()
+    s, o = torch.sigmoid(g), torch.sigmoid(-g)
+    low = 2.0 ** -148
+    h = (v + 5) * U * (g * s * u).abs() + low * (1 + g.abs()) * u.abs()
+    du = (v + 5) * U * (g * s * dh).abs() + low * (1 + g.abs()) * dh.abs()
+    # d = s (1 + g (1 - s)): s's error, that of 1 - s times g, one rounding of the sum and one of the product; then two products
+    inner = 1 + (g * o).abs()
+    dg = ((v + 3) + (v + 4) + 4) * U * (dh * u).abs() * s * inner + low * inner * (dh * u).abs() \
+        + low * torch.minimum(dh.abs(), u.abs())
+    return h, du, dg
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("F", [256, 264, 260, 258, 257])     # 8 values a lane without and with gaps, fours, pairs, single
+def test_swiglu_of_far_gates_and_large_factors(F, dtype):
+    # the sigmoid at -104 to 90 beside factors up to 1e30: a finite result stays finite and keeps its bits,
+    # also where exp(-g) or dh * u pass fp32's range
+    R = 48
+    lo, hi = torch.linspace(-104, 80, R, device="cuda")[:, None], torch.linspace(0, 10, F, device="cuda")
+    g = (lo + hi).to(dtype)
+    top = 4.0 if dtype is F16 else 30.0
+    ten = torch.full((), 10.0, dtype=F64, device="cuda")
+    far = torch.pow(ten, torch.linspace(-4, top, R, device="cuda", dtype=F64))[:, None]
+    u = (rnd(R, F, seed=1).to(F64) * far).to(dtype)
+    dh = (rnd(R, F, seed=2).to(F64) * far.flip(0)[torch.randperm(R, generator=torch.Generator().manual_seed(3))]).to(dtype)
+    u[:8], dh[:8] = (v[:8].to(F64).sign().to(dtype) * float(10 ** top) for v in (u, dh))     # both large where s is least
+    h, kept = moe.moe_swiglu_save(g, u)
+    wide = torch.empty(R, F, device="cuda")
+    gk, uk = (moe.moe_act_load(c, x=wide.clone()).to(F64) for c in (kept.g, kept.u))
+    dg, du, again = moe.moe_swiglu_backward(dh, kept, rebuild_h=True)
+
+    def close(got, want, err):
+        top = torch.finfo(dtype)
+        fits = want.abs() < top.max * (1 - top.eps)
+        assert bool(fits.any())
+        tol = half_step(dtype) * want.abs() + (1 + half_step(dtype)) * err + top.tiny * top.eps / 2
+        return bool((~fits | ((got.to(F64) - want).abs() <= tol)).all())
+
+    def formulas(g, u, dh):
+        s = torch.sigmoid(g)
+        return g * s * u, dh * g * s, dh * u * s * (1 + g * torch.sigmoid(-g))
+
+    d64 = dh.to(F64)
+    want, err = formulas(g.to(F64), u.to(F64), d64), swiglu_errors(g.to(F64), u.to(F64), d64, dtype)
+    assert close(h, want[0], err[0])
+    want, err = formulas(gk, uk, d64), swiglu_errors(gk, uk, d64, dtype)
+    assert close(again, want[0], err[0]) and close(du, want[1], err[1]) and close(dg, want[2], err[2])
