@@ -484,6 +484,17 @@ MOE_API moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64
                                 const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
                                 int64_t ldo, int32_t* status, cudaStream_t stream);
 
+/*
+ * moe_adapters_debug -- moe_adapters with the status word and the test hooks of a moe_debug (NULL: none;
+ *   its other fields are not used).  test_withhold makes the kernel of long batches keep its first
+ *   products' completion back, so that its bounded waits run out after wait_cycles: *status becomes
+ *   MOE_ERR_TIMEOUT, out is undefined and the context stays usable.
+ */
+MOE_API moe_status moe_adapters_debug(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
+                                      int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
+                                      const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
+                                      int64_t ldo, const moe_debug* dbg, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

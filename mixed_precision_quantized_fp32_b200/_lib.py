@@ -25,7 +25,7 @@ STATUS = {
 
 EXPORTS = ("moe_pack", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_sort", "moe_dispatch",
            "moe_dispatch_backward", "moe_collect", "moe_collect_backward", "moe_act_save", "moe_act_load",
-           "moe_swiglu_save", "moe_swiglu_backward", "moe_adapters")
+           "moe_swiglu_save", "moe_swiglu_backward", "moe_adapters", "moe_adapters_debug")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -83,6 +83,8 @@ def load() -> C.CDLL:
             "moe_swiglu_save": [P, i64, P, i64, i32, i32, i32, P, i64, P, P, P, P, P, P],
             "moe_swiglu_backward": [P, i64, i32, P, P, P, P, i32, i32, P, i64, P, i64, P, i64, P, P],
             "moe_adapters": [P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, i64, P, P],
+            "moe_adapters_debug": [P, i64, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, i64,
+                                   C.POINTER(MoeDebug), P],
         }.items():
             fn = getattr(L, name)
             fn.restype, fn.argtypes = C.c_int, args

@@ -447,7 +447,9 @@ __device__ __forceinline__ void tmem_rows16(uint32_t taddr, float (&r)[X][4]) {
 // matrix descriptors say.  Row j of a B stage is output 8*(c/2) + 2*i + c%2 of its half of the
 // 64, with i = j/8 % 4 and c = j % 8, so that a lane of the epilogue has eight outputs in a row.
 // Two blocks share an SM; each asks for 256 of its 512 tensor-memory columns and for more than
-// a third of its shared memory, so that a third block never waits for columns.
+// a third of its shared memory, so that a third block never waits for columns.  Every wait is bounded;
+// where one gives up, all later ones of the block do, and it ends when its MMAs have.  withhold (a test
+// hook): the first stage's completion is not reported.
 constexpr int kWideStages = 5;
 constexpr int kWideAhead = 3;  // stages copied ahead
 constexpr int kWideThreads = kAdThreads + 32;
@@ -472,12 +474,14 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
     adapter_wide_kernel(const T* __restrict__ x, int64_t ldx, const T* y, int64_t ldy, int T_, int K, int N, int r,
                         int n, const T* __restrict__ A, const T* __restrict__ B, const float* __restrict__ scale,
                         const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets, bool rest, int cluster,
-                        int kslice, int nslice, T* out, int64_t ldo, int32_t* status) {
+                        int kslice, int nslice, T* out, int64_t ldo, int32_t* status, long long wait, bool withhold) {
   pdl_enter();  // before any global memory access (see moe_common.cuh)
   constexpr int TM = kWideTokens, RP = NR * 8, KBLK = NR <= 8 ? 1 : 2, HALF = RP / 16;  // HALF: n8 tiles of half of P
   constexpr int STAGE = wide_stage_bytes<NR>();
   extern __shared__ uint8_t wide_sm[];
   __shared__ uint64_t done[kWideStages];  // the MMAs that read a stage have completed
+  __shared__ uint64_t all_done;           // after a wait that gave up: all MMAs have
+  __shared__ uint64_t spare;              // takes the report that withhold keeps from `done`
   __shared__ uint32_t tmem_at;
   __shared__ int given_up;
   const uint32_t ring = (ptx::smem_u32(wide_sm) + 1023u) & ~1023u;  // swizzled tiles start at multiples of 1024
@@ -557,7 +561,7 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
     copy_commit();
   };
   auto wait_done = [&](int st) {  // of the stage's MMAs; bounded
-    if (!ptx::mbar_wait(&done[st % kWideStages], (st / kWideStages) & 1, &given_up, kWideWait)) given_up = 1;
+    if (!ptx::mbar_wait(&done[st % kWideStages], (st / kWideStages) & 1, &given_up, wait)) given_up = 1;
   };
   if (drains) {
 #pragma unroll
@@ -567,6 +571,8 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
     ptx::tmem_relinquish();  // at once: the SM's other block waits for the permit
     if (lane == 0) {
       for (int i = 0; i < kWideStages; ++i) ptx::mbar_init(&done[i], 1);
+      ptx::mbar_init(&all_done, 1);
+      ptx::mbar_init(&spare, 1);
       ptx::fence_mbar_init();
       given_up = 0;
     }
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // 16 values, 32 bytes, at a time
         ptx::mma_f16_ss_warp(tmem, xd + 2 * k, ad + 2 * k, wide_idesc<T>(RP), st || k ? 1u : 0u);
-      ptx::mma_commit_warp(&done[st % kWideStages]);
+      ptx::mma_commit_warp(withhold && st == 0 ? &spare : &done[st % kWideStages]);
     }
   }
   // This block's share of P lies behind the ring's last filled stage: there, unless it is too
@@ -693,15 +699,15 @@ __global__ void __launch_bounds__(kWideThreads, NR <= 8 ? 2 : 1)
   }
   if (up == 0) cluster_wait();
   copy_wait<0>();
-  if (given_up) {  // MMAs may be in flight still: they must not outlive their memory
-    if (tid == 0 && status) *status = MOE_ERR_TIMEOUT;
-    for (int st = max(0, down + up - kWideStages); st < down + up; ++st)
-      ptx::mbar_drain(&done[st % kWideStages], (st / kWideStages) & 1, kWideWait);
-  }
   ptx::tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // all waits are over: given_up stands
+  if (given_up && tid == 0 && status) *status = MOE_ERR_TIMEOUT;
   if (!drains) {
     ptx::tc_fence_after();
+    if (given_up) {  // MMAs may be in flight still, whatever the stages' barriers say: they must not outlive their memory
+      ptx::mma_commit_warp(&all_done);
+      ptx::mbar_drain(&all_done, 0, kWideWait);
+    }
     ptx::tmem_dealloc(tmem, kWideTmem);
   }
 }
@@ -765,7 +771,8 @@ cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
   return launch_cluster(adapter_wide_kernel<T, NR>, dim3((unsigned)p.tiles * p.cluster), dim3(kWideThreads), p.cluster,
                         (size_t)wide_smem_bytes<NR>(), s, (const T*)a.x.p, a.x.ld, (const T*)a.y.p, a.y.ld, a.T, a.K, a.N,
                         a.r, a.n, (const T*)a.A, (const T*)a.B, a.scale, a.perm, a.offsets, a.out.p != a.y.p, p.cluster,
-                        p.kslice, p.nslice, (T*)a.out.p, a.out.ld, a.status);
+                        p.kslice, p.nslice, (T*)a.out.p, a.out.ld, a.status,
+                        a.wait_cycles ? (long long)a.wait_cycles : kWideWait, a.withhold != 0);
 }
 
 // Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of

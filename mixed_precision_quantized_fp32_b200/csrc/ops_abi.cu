@@ -154,10 +154,10 @@ extern "C" moe_status moe_swiglu_backward(const void* dh, int64_t lddh, int32_t 
                                          n_rows, stream));
 }
 
-extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
-                                   int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
-                                   const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
-                                   int64_t ldo, int32_t* status, cudaStream_t stream) {
+static moe_status adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T, int32_t K,
+                           int32_t N, int32_t r, int32_t n, const void* A, const void* B, const float* scale,
+                           const int32_t* perm, const int32_t* offsets, void* out, int64_t ldo, int32_t* status,
+                           uint32_t withhold, uint32_t wait_cycles, cudaStream_t stream) {
   if (!entries_ok(T, 1) || n < 1 || n > kMaxGroups || r < 8 || r > 128 || r % 8 != 0) return MOE_ERR_SHAPE;
   if (!width_ok(K) || !width_ok(N) || K % 8 != 0 || N % 8 != 0) return MOE_ERR_SHAPE;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_FORMAT;
@@ -176,6 +176,23 @@ extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, in
   a.out = {out, ldo};
   a.T = T, a.K = K, a.N = N, a.r = r, a.n = n;
   a.A = A, a.B = B, a.scale = scale, a.perm = perm, a.offsets = offsets;
-  a.status = status;
+  a.status = status, a.withhold = withhold, a.wait_cycles = wait_cycles;
   return launched(launch_adapters(a, dtype, stream));
+}
+
+extern "C" moe_status moe_adapters(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype, int32_t T,
+                                   int32_t K, int32_t N, int32_t r, int32_t n, const void* A, const void* B,
+                                   const float* scale, const int32_t* perm, const int32_t* offsets, void* out,
+                                   int64_t ldo, int32_t* status, cudaStream_t stream) {
+  return adapters(x, ldx, y, ldy, dtype, T, K, N, r, n, A, B, scale, perm, offsets, out, ldo, status, 0, 0, stream);
+}
+
+extern "C" moe_status moe_adapters_debug(const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t dtype,
+                                         int32_t T, int32_t K, int32_t N, int32_t r, int32_t n, const void* A,
+                                         const void* B, const float* scale, const int32_t* perm,
+                                         const int32_t* offsets, void* out, int64_t ldo, const moe_debug* dbg,
+                                         cudaStream_t stream) {
+  const moe_debug d = dbg ? *dbg : moe_debug{};
+  return adapters(x, ldx, y, ldy, dtype, T, K, N, r, n, A, B, scale, perm, offsets, out, ldo, d.status, d.test_withhold,
+                  d.wait_cycles, stream);
 }

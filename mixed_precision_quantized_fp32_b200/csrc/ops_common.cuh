@@ -196,6 +196,7 @@ struct AdapterArgs {
   const float* scale;
   const int32_t *perm, *offsets;
   int32_t* status;  // null, or where MOE_ERR_TIMEOUT goes
+  uint32_t withhold, wait_cycles;  // test hooks (moe_debug.test_withhold / wait_cycles)
 };
 cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t stream);
 

@@ -1,6 +1,8 @@
-"""The operators around the expert products at the ends of their types' ranges.  Tolerances count
+"""The operators around the expert products at the ends of their types' ranges and of their waits.  Tolerances count
 roundings: 2^-24 of the value for one in fp32, half a step of the type for the stored value.
 """
+import ctypes as C
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -10,7 +12,8 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import mixed_precision_quantized_fp32_b200 as moe  # noqa: E402
-from tests.test_gpu_ops import BF16, F16, F32, F64, U, bank, half_step, index, ref_adapters, rnd  # noqa: E402
+from mixed_precision_quantized_fp32_b200 import _lib  # noqa: E402
+from tests.test_gpu_ops import BF16, F16, F32, F64, U, adapters_near, bank, half_step, index, ref_adapters, rnd  # noqa: E402
 
 
 # ------------------------------------------------------------------ adapters: small low-rank terms
@@ -101,3 +104,36 @@ def test_swiglu_of_far_gates_and_large_factors(F, dtype):
     assert close(h, want[0], err[0])
     want, err = formulas(gk, uk, d64), swiglu_errors(gk, uk, d64, dtype)
     assert close(again, want[0], err[0]) and close(du, want[1], err[1]) and close(dg, want[2], err[2])
+
+
+# ------------------------------------------------------------------ adapters: waits that run out
+@pytest.mark.parametrize("K,r", [(40, 16), (264, 64), (2056, 64), (1096, 128)])   # one stage a block to more than the ring holds
+def test_adapters_wait_that_runs_out_is_reported_and_leaves_the_context_usable(K, r):
+    # the kernel of long batches keeps the completion of its first products back and its waits get 200k cycles
+    # (0.1 ms): every block ends by itself, the status says so, and a call after it is right.  A status that
+    # nothing timed out for stays as it was.
+    T, N, n = 2100, 520, 3
+    ids = index(T, 1, n, "holes")[:, 0]
+    x, y = rnd(T, K, dtype=BF16), rnd(T, N, dtype=BF16, seed=1)
+    A, B, scale = bank(n, r, K, N, BF16)
+    routes = moe.moe_sort(ids, n)
+    want, mag = ref_adapters(x, y, A, B, scale, ids)
+    status, out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty_like(y)
+
+    def call(**hooks):
+        d = _lib.MoeDebug(status=status.data_ptr(), **hooks)
+        _lib.check("moe_adapters_debug", _lib.load().moe_adapters_debug(
+            x.data_ptr(), K, y.data_ptr(), N, 0, T, K, N, r, n, A.data_ptr(), B.data_ptr(), scale.data_ptr(),
+            routes.perm.data_ptr(), routes.offsets.data_ptr(), out.data_ptr(), N, C.byref(d),
+            torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        return _lib.STATUS[int(status)]
+
+    assert call() == "MOE_OK" and adapters_near(out, want, mag, K, r, BF16)
+    assert call(test_withhold=1, wait_cycles=200_000) == "MOE_ERR_TIMEOUT"
+    status.zero_()
+    for _ in range(3):
+        out.zero_()
+        assert call() == "MOE_OK" and adapters_near(out, want, mag, K, r, BF16)
+    again = moe.moe_adapters(x, y, A, B, scale, routes, status=status)
+    assert torch.equal(again, out) and int(status) == 0
