@@ -61,21 +61,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _bind_command() -> tuple[list[str], str]:
+    """The binding's compile command, and what its object depends on besides the sources: torch's
+    and Python's versions (it uses internal headers of both) and the command itself."""
+    import importlib.metadata
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-I", os.path.join(ROOT, "include"), *(a for i in inc for a in ("-isystem", i)), BIND_SRC,
+           "-o", BIND_LIB + ".tmp", "-L", HERE, "-l:libmoe_b200.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return cmd, "\n".join([importlib.metadata.version("torch"), sys.version, *cmd])
+
+
 def build_bind(force: bool = False) -> str:
     """The operators' native Python calls; loads libmoe_b200.so from its own folder."""
-    if force or _stale(BIND_LIB, [BIND_SRC, os.path.join(ROOT, "include", "moe.h")]):
-        import importlib.util
-        import sysconfig
-        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-        cuda = os.path.dirname(os.path.dirname(NVCC))
-        inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-        subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-                        "-I", os.path.join(ROOT, "include"), *(a for i in inc for a in ("-isystem", i)), BIND_SRC,
-                        "-o", BIND_LIB + ".tmp", "-L", HERE, "-l:libmoe_b200.so", "-Wl,-rpath,$ORIGIN",
-                        "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda",
-                        "-lc10"], check=True)
+    cmd, key = _bind_command()
+    stamp = os.path.join(BUILD, "bind.key")
+    built_of = open(stamp).read() if os.path.exists(stamp) else None
+    if force or built_of != key or _stale(BIND_LIB, [BIND_SRC, os.path.join(ROOT, "include", "moe.h")]):
+        os.makedirs(BUILD, exist_ok=True)
+        subprocess.run(cmd, check=True)
         os.replace(BIND_LIB + ".tmp", BIND_LIB)
+        with open(stamp, "w") as f:
+            f.write(key)
     return BIND_LIB
 
 

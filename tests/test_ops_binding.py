@@ -1,7 +1,10 @@
 """Host-side checks of the operators' entry points beyond their arguments' ranges (no GPU needed)."""
 import ctypes as C
+import importlib.metadata
+import os
 
 from mixed_precision_quantized_fp32_b200 import _lib
+from mixed_precision_quantized_fp32_b200 import build as bld
 from tests.test_ops_host import ARGS, FAKE, OK, no_gpu
 
 
@@ -21,3 +24,34 @@ def test_adapters_debug_refuses_what_adapters_refuses():
 @no_gpu
 def test_adapters_debug_without_hooks_reaches_the_device_check():
     assert debug_call() in OK and debug_call(C.byref(_lib.MoeDebug(status=FAKE))) in OK
+
+
+# ------------------------------------------------------------------ what the binding's object is built of
+def test_binding_is_rebuilt_when_torch_python_or_the_command_change(tmp_path, monkeypatch):
+    # it is compiled against internal headers of torch and Python: an object of other versions may not load
+    lib = str(tmp_path / "bind.so")
+    ran = []
+
+    def compile_(cmd, check):
+        ran.append(cmd)
+        open(lib + ".tmp", "w").close()
+
+    monkeypatch.setattr(bld, "BIND_LIB", lib)
+    monkeypatch.setattr(bld, "BUILD", str(tmp_path / "objects"))
+    monkeypatch.setattr(bld.subprocess, "run", compile_)
+
+    def runs():
+        ran.clear()
+        assert bld.build_bind() == lib and os.path.exists(lib)
+        return len(ran)
+
+    assert runs() == 1 and runs() == 0
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0" if name == "torch" else version(name))
+    assert runs() == 1 and runs() == 0
+    monkeypatch.setattr(bld.sys, "version", "another Python")
+    assert runs() == 1 and runs() == 0
+    monkeypatch.setattr(bld, "NVCC", "/elsewhere/bin/nvcc")        # other headers
+    assert runs() == 1 and runs() == 0
+    os.utime(lib, (1, 1))                                          # older than its source
+    assert runs() == 1
