@@ -48,7 +48,10 @@ bool none(PyObject* o) { return o == Py_None; }
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(name, " must be a tensor, got ", Py_TYPE(o)->tp_name);
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // its memory holds the values with the other sign
+  if (t.is_neg()) refuse(name, " is negated lazily: pass its resolve_neg()");
+  return t;
 }
 
 int32_t integer(PyObject* o, const char* name) {

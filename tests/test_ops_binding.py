@@ -3,6 +3,10 @@ import ctypes as C
 import importlib.metadata
 import os
 
+import pytest
+import torch
+
+import mixed_precision_quantized_fp32_b200 as moe
 from mixed_precision_quantized_fp32_b200 import _lib
 from mixed_precision_quantized_fp32_b200 import build as bld
 from tests.test_ops_host import ARGS, FAKE, OK, no_gpu
@@ -55,3 +59,34 @@ def test_binding_is_rebuilt_when_torch_python_or_the_command_change(tmp_path, mo
     assert runs() == 1 and runs() == 0
     os.utime(lib, (1, 1))                                          # older than its source
     assert runs() == 1
+
+
+# ------------------------------------------------------------------ tensors whose memory is not their value
+T, K2, E, H = 4, 2, 3, 8
+
+
+def calls():
+    """Every call with its arguments by name, all tensors on the CPU (which each call refuses by itself)."""
+    x, i, w = torch.zeros(T, H), torch.zeros(T, K2, dtype=torch.int32), torch.zeros(T, K2)
+    r = moe.Routes(T, K2, E, i[:, 0], i[:, 0], i[:, 0])
+    c = moe.ActCkpt(torch.zeros(T, H, dtype=torch.int8), torch.zeros(T, 1, dtype=torch.uint8), torch.float32)
+    return {
+        "dispatch": (lambda x: moe.moe_dispatch(x, i, E), dict(x=x)),
+        "dispatch_backward": (lambda dxs: moe.moe_dispatch_backward(dxs, r), dict(dxs=x)),
+        "collect": (lambda o: moe.moe_collect(o, w, r), dict(o=x)),
+        "collect_backward": (lambda dy, o: moe.moe_collect_backward(dy, o, w, r), dict(dy=x, o=x)),
+        "act_save": (lambda x: moe.moe_act_save(x), dict(x=x)),
+        "swiglu_save": (lambda g, u: moe.moe_swiglu_save(g, u), dict(g=x, u=x)),
+        "swiglu_backward": (lambda dh: moe.moe_swiglu_backward(dh, moe.SwigluCkpt(c, c)), dict(dh=x)),
+        "adapters": (lambda x, y, A, B: moe.moe_adapters(x, y, A, B, w[:, 0], r), dict(x=x, y=x, A=x, B=x)),
+    }
+
+
+@pytest.mark.parametrize("name", calls())
+def test_lazily_negated_views_are_refused(name):
+    call, args = calls()[name]
+    with pytest.raises(ValueError, match="cuda"):
+        call(**args)
+    for key in args:
+        with pytest.raises(ValueError, match=f"{key} is negated"):
+            call(**dict(args, **{key: torch._neg_view(args[key])}))
