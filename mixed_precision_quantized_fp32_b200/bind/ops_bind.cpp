@@ -8,6 +8,8 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -15,6 +17,7 @@
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <climits>
@@ -46,11 +49,21 @@ std::string shape_of(const at::Tensor& t) {
 
 bool none(PyObject* o) { return o == Py_None; }
 
+// Whether autograd records what is computed from t: the result would silently be cut off from it.
+bool recorded(const at::Tensor& t) {
+  if (!torch::autograd::impl::get_autograd_meta(t)) return false;  // most tensors
+  if (c10::GradMode::is_enabled() && t.requires_grad()) return true;
+  return c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined();
+}
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(name, " must be a tensor, got ", Py_TYPE(o)->tp_name);
   const at::Tensor& t = THPVariable_Unpack(o);
   // its memory holds the values with the other sign
   if (t.is_neg()) refuse(name, " is negated lazily: pass its resolve_neg()");
+  if (recorded(t))
+    refuse(name, " takes part in a gradient, which this call does not record: make it under torch.no_grad(), or in a "
+                 "torch.autograd.Function whose backward makes the gradient's call");
   return t;
 }
 

@@ -10,7 +10,9 @@ current one.  Outputs may be given; otherwise they are allocated on the stream o
 Outputs must not overlap inputs unless a call says so.  Calls run asynchronously on ``stream``
 (default: the device's current stream) and can be captured into a CUDA graph.  A tensor that
 does not fit raises ValueError, what the C ABI refuses MoeError.  The operators record
-nothing for autograd: each gradient is a call of its own.
+nothing for autograd: each gradient is a call of its own, and where autograd would record, a
+tensor that takes part in a gradient raises ValueError (call under ``torch.no_grad()``, or in
+a ``torch.autograd.Function`` that makes both calls).
 """
 from __future__ import annotations
 

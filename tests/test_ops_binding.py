@@ -61,7 +61,7 @@ def test_binding_is_rebuilt_when_torch_python_or_the_command_change(tmp_path, mo
     assert runs() == 1
 
 
-# ------------------------------------------------------------------ tensors whose memory is not their value
+# ------------------------------------------------------------------ tensors that are more than their memory
 T, K2, E, H = 4, 2, 3, 8
 
 
@@ -90,3 +90,45 @@ def test_lazily_negated_views_are_refused(name):
     for key in args:
         with pytest.raises(ValueError, match=f"{key} is negated"):
             call(**dict(args, **{key: torch._neg_view(args[key])}))
+
+
+@pytest.mark.parametrize("name", calls())
+def test_tensors_that_take_part_in_a_gradient_are_refused_where_it_would_be_lost(name):
+    import torch.autograd.forward_ad as fwd
+    call, args = calls()[name]
+    for key in args:
+        leaf = dict(args, **{key: args[key].clone().requires_grad_()})
+        inner = dict(args, **{key: leaf[key] * 2})
+        for a in (leaf, inner):
+            with pytest.raises(ValueError, match=f"{key} takes part in a gradient"):
+                call(**a)
+            for quiet in (torch.no_grad, torch.inference_mode):
+                with quiet(), pytest.raises(ValueError, match="cuda"):     # as without one
+                    call(**a)
+        with fwd.dual_level():
+            dual = fwd.make_dual(args[key], torch.ones_like(args[key]))
+            with pytest.raises(ValueError, match=f"{key} takes part in a gradient"):
+                call(**dict(args, **{key: dual}))
+        with pytest.raises(ValueError, match="cuda"):
+            call(**dict(args, **{key: leaf[key].detach()}))
+
+
+def test_the_body_of_an_autograd_function_is_not_refused():
+    call, args = calls()["collect"]
+
+    class Collect(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, o):
+            with pytest.raises(ValueError, match="cuda"):
+                call(o=o)
+            return o.clone()
+
+        @staticmethod
+        def backward(ctx, g):
+            with pytest.raises(ValueError, match="cuda"):
+                call(o=g)
+            return g
+
+    o = args["o"].clone().requires_grad_()
+    Collect.apply(o).sum().backward()
+    assert torch.equal(o.grad, torch.ones_like(o))
