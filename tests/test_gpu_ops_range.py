@@ -137,3 +137,58 @@ def test_adapters_wait_that_runs_out_is_reported_and_leaves_the_context_usable(K
         assert call() == "MOE_OK" and adapters_near(out, want, mag, K, r, BF16)
     again = moe.moe_adapters(x, y, A, B, scale, routes, status=status)
     assert torch.equal(again, out) and int(status) == 0
+
+
+# ------------------------------------------------------------------ adapters: every bit
+SHAPES = [(1, 4096, 4096, 16, 3), (40, 1032, 264, 8, 3), (130, 4096, 520, 32, 4), (64, 4104, 2000, 120, 2), (300, 2056, 1096, 64, 2),
+          (128, 136, 520, 56, 5), (260, 1000, 40, 24, 40),                                            # tiles of 16 tokens
+          (2100, 1096, 520, 32, 5), (2100, 8, 72, 8, 3), (2060, 2056, 328, 40, 2), (2049, 4104, 2000, 120, 1), (2500, 1000, 72, 128, 9),
+          (1100, 2056, 1096, 64, 2)]                                                                   # and of 64
+
+
+def whole(shape, top, seed):
+    return torch.randint(-top, top + 1, shape, generator=torch.Generator().manual_seed(seed + sum(shape)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,K,N,r,n", SHAPES)
+def test_adapters_are_exact_where_every_sum_is(T, K, N, r, n, dtype):
+    # whole numbers: A x needs up to 16 bits, more than the type has, and the outputs are differences of two of
+    # its elements, which are small.  Rows 2i and 2i+1 of A differ by one at the places k = i mod r/2, so
+    # a bit of A x that is lost, or a k, an element of the rank or a block's share left out, shows in the outputs.
+    ids = index(T, 1, n, "holes" if T > 1 else "all")[:, 0]
+    x = whole((T, K), 1, 1).to(dtype)
+    A = whole((n, r // 2, 1, K), 126, 2).expand(n, r // 2, 2, K).clone()
+    pair = torch.arange(K) % (r // 2)
+    A[:, pair, 1, torch.arange(K)] += 2 * whole((n, K), 1, 3).ne(0) - 1
+    A = A.reshape(n, r, K).to(dtype)
+    take = torch.zeros(n, N, r // 2)
+    for seed in (4, 5):                          # each output takes two pairs, with either sign
+        at = torch.randint(0, r // 2, (n, N, 1), generator=torch.Generator().manual_seed(seed + N))
+        take.scatter_(2, at, (2 * (whole((n, N, 1), 1, seed) > 0) - 1).float())
+    B = torch.stack([take, -take], 3).reshape(n, N, r).to(dtype)
+    y, scale = whole((T, N), 8, 6).to(dtype), torch.tensor([1.0, 0.5, -1.0, 2.0])[torch.arange(n) % 4]
+    x, A, B, y, scale = (t.cuda() for t in (x, A, B, y, scale))
+    routes = moe.moe_sort(ids, n)
+    want, _ = ref_adapters(x, y, A, B, scale, ids)
+    P = torch.stack([x.to(F64) @ a.to(F64).T for a in A])
+    # P in 16 bits, so that its two terms hold all of it (and more than the type's bits); results in the type's
+    assert float(P.abs().max()) < 2 ** 15 and (K < 100 or float(P.abs().max()) > 2 ** 11)
+    assert torch.equal(want.to(dtype).to(F64), want) and float((want - y.to(F64)).abs().max()) >= 1
+    assert torch.equal(moe.moe_adapters(x, y, A, B, scale, routes).to(F64), want)
+    z = y.clone()
+    assert torch.equal(moe.moe_adapters(x, z, A, B, scale, routes, out=z).to(F64), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,K,N,r,n", SHAPES)
+def test_adapters_as_a_whole(T, K, N, r, n, dtype):
+    # the term alone (y = 0), over all outputs: each is off by at most half a step of itself, by P's two terms
+    # (2^-17 of each product) and by fp32 sums, whose errors, about 2^-24 times a few, are far below 2^-14 of their root mean square
+    ids = index(T, 1, n, "all")[:, 0]
+    x, y = rnd(T, K, dtype=dtype), torch.zeros(T, N, dtype=dtype, device="cuda")
+    A, B, scale = bank(n, r, K, N, dtype)
+    want, _ = ref_adapters(x, y, A, B, scale, ids)
+    err = moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, n)).to(F64) - want
+    rms = lambda t: float(t.square().mean().sqrt())  # noqa: E731
+    assert rms(err) <= (half_step(dtype) + 2.0 ** -14) * rms(want)
