@@ -459,10 +459,11 @@ constexpr int kWideTile = 64 * 128;  // 64 rows of 128 bytes
 
 template <int NR> constexpr int wide_stage_bytes() { return kWideTile + (NR <= 8 ? kWideTile : 2 * kWideTile); }
 template <int NR> constexpr int wide_smem_bytes() {
-  const int need = 1024 + kWideStages * wide_stage_bytes<NR>() + 2 * (NR <= 8 ? 1 : 2) * kWideTile + kWideTokens * 4 +
-                   (NR <= 8 ? 0 : kWideTokens * NR * 8 * 4);
-  return need < 80 * 1024 ? 80 * 1024 : need;
+  return 1024 + kWideStages * wide_stage_bytes<NR>() + 2 * (NR <= 8 ? 1 : 2) * kWideTile + kWideTokens * 4 +
+         (NR <= 8 ? 0 : kWideTokens * NR * 8 * 4);
 }
+
+static_assert(wide_smem_bytes<4>() > 76 * 1024, "two blocks an SM, not three");
 
 template <typename T> __host__ __device__ constexpr uint32_t wide_idesc(int N) {
   const uint32_t type = is_f16<T> ? 0u : 1u;  // of A and of B

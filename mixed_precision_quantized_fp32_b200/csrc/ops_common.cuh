@@ -149,7 +149,6 @@ inline cudaError_t launch_cluster(void (*kern)(Exp...), dim3 grid, dim3 block, i
 }
 
 inline int dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
-inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // A row-major matrix as the operators take it: `ld` values from one row to the next.
 struct ConstRows {
