@@ -742,7 +742,7 @@ cudaError_t allow_smem(Kern kern, int smem) {
 // tokens of 2 adapters, K = N = 2048, r 128, 4 blocks a tile 11.7 us, 8 14.2; 600 of 8, 4096 ->
 // 1000, r 64, 2 blocks 11.3, 8 15.9; 100 of 60, 2048, r 32, 4 blocks 7.2, 8 8.4).  Two an SM, and a
 // tenth more since some tokens have no adapter, at ranks up to 16, where latency counts for more
-// (K = N = 4096, r 16: 1024 tokens of 32 adapters 17.8 us with 2 blocks a tile, 11.8 with 4; 64 of 48
+// (K = N = 4096, r 16: 1024 tokens of 32 adapters 17.8 us with 2 blocks a tile, 12.0 with 4; 64 of 48
 // 7.8 with 4, 6.3 with 8), and where each tile brings much of an adapter of its own from memory
 // (64 of 48, r 64: 14.9 with 4, 10.9 with 8).
 template <typename T, int NR>
@@ -763,7 +763,8 @@ cudaError_t adapters_short(const AdapterArgs& a, cudaStream_t s) {
 }
 // 64-token tiles: as many as an SM holds.  8192 tokens of 24 adapters, r 64, take 31.2 us with 2
 // blocks a tile and 37.6 with 1; of 32 adapters, r 128, one block an SM, 42.8 with 1 and 49.7 with 2;
-// 2048 tokens of 16, K = N = 4096, r 64, 29.0 with 4 and 33.6 with 8, more than fit.
+// 2048 tokens of 16, K = N = 4096, r 64, each token with one of them, 29.3 with 4 and 33.6 with 8, more
+// than fit.
 template <typename T, int NR>
 cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
   const Shares p = shares_of(a, kWideTokens, 64, [](int blocks, int) { return blocks <= 148 * (NR <= 8 ? 2 : 1); });
@@ -778,13 +779,17 @@ cudaError_t adapters_wide(const AdapterArgs& a, cudaStream_t s) {
 
 // Tiles of 16 tokens where every row may be a request of its own (decode batches, banks of
 // many adapters) and where there is little to multiply; tiles of 64 where adapters have rows
-// enough to fill them.  16- against 64-token tiles (T, K, N, r, adapters):
-//   350, 2896, 2896, 96, 1    13.8 / 16.8 us       2048, 1024, 1024, 64, 16   11.7 / 10.4
-//   512, 2048, 2048, 128, 4   11.9 / 16.3          2048, 2048, 2048, 32, 16   17.4 / 13.6
-//   1024, 2048, 2048, 64, 8   11.8 / 14.3          1000, 4096, 4096, 32, 8    17.0 / 15.4
-//   1024, 4096, 4096, 16, 32  12.4 / 16.7          8192, 256, 256, 64, 24     15.7 / 10.6
-//   2048, 1024, 1024, 32, 16   8.3 /  9.4          2048, 4096, 4096, 64, 16   43.9 / 24.5
-//   512, 4096, 4096, 16, 64   10.5 / 22.5          8192, 128, 128, 8, 24       9.8 / 8.1
+// enough to fill them.  16- against 64-token tiles (T, K, N, r, adapters; a few requests more than
+// adapters, of which an eighth has none):
+//   350, 2896, 2896, 96, 1    13.8 / 16.9 us       2048, 1024, 1024, 64, 16   11.8 / 10.8
+//   512, 2048, 2048, 128, 4   11.8 / 16.4          2048, 2048, 2048, 32, 16   17.3 / 13.3
+//   1024, 2048, 2048, 64, 8   11.8 / 14.5          1000, 4096, 4096, 32, 8    16.7 / 15.6 (*)
+//   1024, 4096, 4096, 16, 32  12.0 / 16.3          8192, 256, 256, 64, 24     15.7 / 10.7
+//   2048, 1024, 1024, 32, 16   8.6 /  9.5          2048, 4096, 4096, 64, 16   42.9 / 24.3
+//   512, 4096, 4096, 16, 64   10.4 / 22.2          8192, 128, 128, 8, 24       9.8 / 8.2
+// The rule is two cuts through these points, and time moves in waves of blocks.  It takes the slower side at
+// (*), and where every token has an adapter at 512, 2048, 2048, 128, 4 (20.8 / 17.3, the 16-token tiles
+// just beyond one wave) and 640 or 800, 4096, 4096, 32, 4 to 8 (18.2 / 15): up to a fifth more.
 template <typename T>
 cudaError_t adapters_of(const AdapterArgs& a, cudaStream_t s) {
   const int64_t products = (int64_t)a.T * a.r * (a.K + a.N);

@@ -22,7 +22,7 @@
 //   save and load, 8192 x 4096 bf16 (203 MB)               31.2 us, 101%
 //   SwiGLU forward and backward, 4096 x 14336 bf16 (1.06 GB)  162 us, 102%
 //   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 47, 49, 68 us
-//   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 81, 114 us (81, 71, 50%)
+//   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 82, 115 us (81, 70, 50%)
 #include <initializer_list>
 #include <type_traits>
 
@@ -684,7 +684,7 @@ dim3 grid_of(Way w, int R, int F, int span) {
 }
 
 // SwiGLU of pairs and fours: S = 2 where there are groups enough for all warps the machine holds
-// (4096 x 5002 bf16 81 us, S = 1 92), else 1 (1000 x 1022 7.3 us, S = 2 8.4; 333 x 778 fp32 4.3 / 5.0).
+// (4096 x 5002 bf16 82 us, S = 1 92), else 1 (1000 x 1022 7.3 us, S = 2 8.4; 333 x 778 fp32 4.3 / 5.0).
 bool long_spans(int R, int F) { return (int64_t)R * ((F + kGroup - 1) / kGroup) >= 1 << 17; }
 int swiglu_span(Way w, int R, int F) { return w == Way::kOne || !long_spans(R, F) ? 4 : 8; }
 
