@@ -22,7 +22,7 @@
 //   save and load, 8192 x 4096 bf16 (203 MB)               31.2 us, 101%
 //   SwiGLU forward and backward, 4096 x 14336 bf16 (1.06 GB)  162 us, 102%
 //   widths in fours, in pairs and odd: save and load of 8192 x 4092, 4094, 4095 47, 49, 68 us
-//   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 82, 115 us (81, 70, 50%)
+//   (67, 64, 46%), SwiGLU of 4096 x 5004, 5002, 5001 71, 82, 113 us (81, 70, 51%)
 #include <initializer_list>
 #include <type_traits>
 
@@ -153,9 +153,10 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t eb, float (&v)[8]) {
   decode<8>(q, eb, v);
 }
 
-// Arithmetic on one value or on two, which share an instruction (f32x2).  The kernels with eight values a
-// lane take pairs: what they have to compute for a value takes as long as its bytes (backward of
-// 4096 x 14336 bf16 92 us, with single values 96).
+// Arithmetic on one value or on two, which share an instruction (f32x2).  What there is to compute for a
+// value takes as long as its bytes, so pairs are taken (backward of 4096 x 14336 bf16 92 us, with single
+// values 96; forward of 4096 x 5001 bf16 54, 56), but for the backward pass with fewer than eight values
+// a lane, which they do not help (4096 x 5002 bf16: 52 us for 47).
 __device__ __forceinline__ uint64_t join(float2 v) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) swiglu_backward_k
 // S times, with all loads in flight, and finds the row once.  The number of instructions bounds
 // these kernels, and few lanes a group save what each of them computes for it; but a larger N
 // spreads an access over more lines.  Single values: save and load of 8192 x 4095 bf16 take 68 us
-// with N = 2 (1: 76, 4: 71); the SwiGLU kernels, with more to do for a value, 114 for 4096 x 5001
+// with N = 2 (1: 76, 4: 71); the SwiGLU kernels, with more to do for a value, 113 for 4096 x 5001
 // with N = 1 (4: 135).  Pairs take N = 4: save and load of 8192 x 4094 49 us, with N = 2 58.
 template <int V> constexpr int kMany = V == 1 ? 2 : 4;  // N of save and load
 template <int V> constexpr int kSpan = 8 / kMany<V>;    // their S
@@ -616,9 +617,11 @@ __global__ void __launch_bounds__(256) swiglu_save_v_kernel(const T* __restrict_
   encode_span<T, V>(a, s.left, gq + at, ge + e_at);
   encode_span<T, V>(b, s.left, uq + at, ue + e_at);
 #pragma unroll
-  for (int i = 0; i < S; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) a[i][j] = swiglu<T>(a[i][j], b[i][j]);
+  for (int i = 0; i < S * N; i += 2) {
+    float &p = a[i / N][i % N], &q = a[(i + 1) / N][(i + 1) % N];
+    const float2 y = swiglu<T>(make_float2(p, q), make_float2(b[i / N][i % N], b[(i + 1) / N][(i + 1) % N]));
+    p = y.x, q = y.y;
+  }
   store_span<V>(h + s.row * ldh + s.col, s.left, a);
 }
 
