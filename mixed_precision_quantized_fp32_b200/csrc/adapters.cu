@@ -145,12 +145,14 @@ __device__ void copy_rest(const T* y, int64_t ldy, T* out, int64_t ldo, int N, i
   }
 }
 
-// Two values as hi and lo terms of T; an infinity stays one (inf - inf would be NaN).
+// Two values as hi and lo terms of T.  hi stays finite: a finite value next to T's largest would round to an
+// infinity, and an infinity goes to lo alone (inf - inf would be NaN), where a NaN goes too.
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack2<T>(a, b);
+  constexpr float top = is_f16<T> ? 65504.0f : 0x1.FEp127f;
+  hi = pack2<T>(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
   const float2 f = unpack2<T>(hi);
-  lo = pack2<T>(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
+  lo = pack2<T>(a - f.x, b - f.y);
 }
 
 // The power of two 2^-e that brings a row of P, whose largest magnitude has these bits, into

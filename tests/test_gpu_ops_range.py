@@ -192,3 +192,32 @@ def test_adapters_as_a_whole(T, K, N, r, n, dtype):
     err = moe.moe_adapters(x, y, A, B, scale, moe.moe_sort(ids, n)).to(F64) - want
     rms = lambda t: float(t.square().mean().sqrt())  # noqa: E731
     assert rms(err) <= (half_step(dtype) + 2.0 ** -14) * rms(want)
+
+
+# ------------------------------------------------------------------ adapters: the largest low-rank terms
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,r", [(40, 16), (300, 128), (2100, 32), (2100, 128)])      # tiles of 16 and of 64 tokens
+def test_adapters_of_the_largest_terms(T, r, dtype):
+    # scale * A x at fp32's largest numbers, which the value type rounds to an infinity, beside a B that brings
+    # them back: the outputs are finite.  An infinity and a NaN stay what they are.
+    K, N = 64, 40
+    x, y = torch.zeros(T, K, dtype=dtype, device="cuda"), torch.zeros(T, N, dtype=dtype, device="cuda")
+    x[:, 0], x[1::2, 0] = 1.0, -1.0
+    A, B = torch.zeros(1, r, K, dtype=dtype, device="cuda"), torch.zeros(1, N, r, dtype=dtype, device="cuda")
+    A[0, 0, 0], A[0, 1, 1] = 1.0, 2.0
+    low = 2.0 ** (-100 if dtype is BF16 else -24)
+    B[0, :, 0] = low
+    B[0, :, 1] = torch.tensor([low, -low], device="cuda").repeat(N // 2)
+    x[5, 1], x[6, 1], x[7, 1] = 1.0, float("nan"), -1.0       # 2 * scale: beyond fp32
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    out = moe.moe_adapters(x, y, A, B, torch.full((1,), torch.finfo(F32).max, device="cuda"), moe.moe_sort(ids, 1)).to(F64)
+    inf = float("inf")
+    want = x[:, :1].to(F64) * torch.finfo(F32).max * low + torch.zeros(N, dtype=F64, device="cuda")
+    want[5, ::2], want[5, 1::2], want[7, ::2], want[7, 1::2] = inf, -inf, -inf, inf
+    if dtype is F16:
+        want[want.abs() > 65504] *= inf          # 2^104: beyond the type, with its sign
+    rest = torch.arange(T, device="cuda") != 6
+    assert bool(torch.isnan(out[6]).all())
+    # P's terms leave 2^-17 of it, and the product with a power of two is exact
+    near = (out - want).abs() <= (half_step(dtype) + 2.0 ** -16) * want.abs()
+    assert bool(((out == want) | (torch.isfinite(want) & near))[rest].all())
